@@ -27,6 +27,13 @@ EQCONV_ERR_DEVICE_CHECK = 5
 EQCONV_DETERMINISTIC = 1
 EQCONV_OUT_ALL_PARITY = 1
 EQCONV_OUT_PER_PATH = 2
+EQCONV_F32 = 0
+EQCONV_BF16 = 1
+EQCONV_F16 = 2
+EQCONV_GATE_NONE = 0
+EQCONV_GATE_SIGMOID = 1
+EQCONV_GATE_SILU = 2
+EQCONV_GATE_TANH = 3
 
 ABI_FUNCTIONS = (
     "eqconv_plan_create", "eqconv_plan_set_vec", "eqconv_plan_info", "eqconv_enumerate_paths", "eqconv_cg_table",
@@ -42,6 +49,10 @@ ABI_FUNCTIONS = (
     "eqconv_backward_radial_workspace_bytes", "eqconv_backward_radial",
     "eqconv_symmetric_contraction_plan_create", "eqconv_symmetric_contraction",
     "eqconv_symmetric_contraction_workspace_bytes", "eqconv_symmetric_contraction_backward",
+    "eqconv_embedding_plan_create", "eqconv_embedding", "eqconv_embedding_workspace_bytes",
+    "eqconv_embedding_backward", "eqconv_block_norm_plan_create", "eqconv_block_norm",
+    "eqconv_block_norm_workspace_bytes", "eqconv_block_norm_backward", "eqconv_clip_workspace_bytes",
+    "eqconv_gradient_norm", "eqconv_clip_gradients",
 )
 
 
@@ -61,12 +72,18 @@ class eqconv_graph_t(ctypes.Structure):
                 ("send_ptr", ctypes.c_void_p), ("send_perm", ctypes.c_void_p)]
 
 
+class eqconv_tensor_t(ctypes.Structure):
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("type", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 _lib = None
 _lock = threading.Lock()
 _vp, _ci, _cu, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint, ctypes.c_size_t
 _pi = ctypes.POINTER(ctypes.c_int)
 _pd = ctypes.POINTER(ctypes.c_double)
 _pg = ctypes.POINTER(eqconv_graph_t)
+_i64, _cf = ctypes.c_int64, ctypes.c_float
 
 _SIGS = {
     "eqconv_plan_create": (_ci, [ctypes.POINTER(_vp), ctypes.c_char_p, _ci, ctypes.c_char_p, _ci]),
@@ -103,6 +120,17 @@ _SIGS = {
     "eqconv_backward_radial": (_ci, [_vp, _pg] + [_vp] * 5 + [_ci, ctypes.c_float] + [_vp] * 7 + [_sz, _vp]),
     "eqconv_forward_radial": (_ci, [_vp, _pg] + [_vp] * 5 + [_ci, ctypes.c_float, _vp, _vp, _sz, _vp]),
     "eqconv_radial_weights": (_ci, [_vp, _ci] + [_vp] * 4 + [_ci, ctypes.c_float, _vp, _vp, _sz, _vp]),
+    "eqconv_embedding_plan_create": (_ci, [ctypes.POINTER(_vp), _i64, _ci, _ci, _ci, _i64]),
+    "eqconv_embedding": (_ci, [_vp, _i64, _vp, _ci, _vp, _i64, _cf, _vp, _i64, _vp]),
+    "eqconv_embedding_workspace_bytes": (_sz, [_vp, _i64]),
+    "eqconv_embedding_backward": (_ci, [_vp, _i64, _vp, _ci, _vp, _i64, _cf, _vp, _vp, _sz, _vp]),
+    "eqconv_block_norm_plan_create": (_ci, [ctypes.POINTER(_vp), ctypes.c_char_p, _ci, _ci, _ci, _cf]),
+    "eqconv_block_norm": (_ci, [_vp, _ci] + [_vp] * 5 + [_cf] + [_vp] * 4),
+    "eqconv_block_norm_workspace_bytes": (_sz, [_vp, _ci]),
+    "eqconv_block_norm_backward": (_ci, [_vp, _ci] + [_vp] * 5 + [_cf] + [_vp] * 9 + [_sz, _vp]),
+    "eqconv_clip_workspace_bytes": (_sz, [_ci, _vp]),
+    "eqconv_gradient_norm": (_ci, [_ci, _vp, _vp, _vp, _sz, _vp]),
+    "eqconv_clip_gradients": (_ci, [_ci, _vp, _cf, _cf, _vp, _vp, _sz, _vp]),
     "eqconv_get_device_error": (_ci, [_vp, _vp, _pi]),
     "eqconv_plan_destroy": (None, [_vp]),
     "eqconv_status_string": (ctypes.c_char_p, [_ci]),
@@ -388,6 +416,71 @@ def eqconv_symmetric_contraction_backward(plan: int, N: int, A, species, W1, W2,
                                                        _ptr(dW2, f), _ptr(workspace), int(workspace_bytes),
                                                        _stream(stream)),
            "eqconv_symmetric_contraction_backward")
+
+
+def eqconv_embedding_plan_create(n_types: int, C: int, table_type: int, out_type: int, padding: int = -1) -> int:
+    h = _vp()
+    _check(lib().eqconv_embedding_plan_create(ctypes.byref(h), int(n_types), int(C), int(table_type), int(out_type),
+                                              int(padding)), "eqconv_embedding_plan_create")
+    return h.value
+
+
+def eqconv_embedding(plan: int, N: int, ids, id_bits: int, table, table_stride: int, scale: float, y, y_stride: int,
+                     stream=None) -> None:
+    """ids, table and y as device pointers (rows table_stride, y_stride elements apart)."""
+    _check(lib().eqconv_embedding(plan, N, ids, id_bits, table, table_stride, scale, y, y_stride, _stream(stream)),
+           "eqconv_embedding")
+
+
+def eqconv_embedding_workspace_bytes(plan: int, N: int) -> int:
+    return int(lib().eqconv_embedding_workspace_bytes(plan, int(N)))
+
+
+def eqconv_embedding_backward(plan: int, N: int, ids, id_bits: int, gy, gy_stride: int, scale: float, dtable,
+                              workspace, workspace_bytes: int, stream=None) -> None:
+    _check(lib().eqconv_embedding_backward(plan, N, ids, id_bits, gy, gy_stride, scale, dtable, _ptr(workspace),
+                                           workspace_bytes, _stream(stream)), "eqconv_embedding_backward")
+
+
+def eqconv_block_norm_plan_create(irreps: str, C: int, type_: int, gate: int, eps: float) -> int:
+    h = _vp()
+    _check(lib().eqconv_block_norm_plan_create(ctypes.byref(h), irreps.encode(), int(C), int(type_), int(gate),
+                                               float(eps)), "eqconv_block_norm_plan_create")
+    return h.value
+
+
+def eqconv_block_norm(plan: int, N: int, x, b, gate, w_post, w_pre, scale: float, x_out, h, stats,
+                      stream=None) -> None:
+    """Tensors as device pointers or None (see include/eqconv.h)."""
+    _check(lib().eqconv_block_norm(plan, N, x, b, gate, w_post, w_pre, scale, x_out, h, stats, _stream(stream)),
+           "eqconv_block_norm")
+
+
+def eqconv_block_norm_workspace_bytes(plan: int, N: int) -> int:
+    return int(lib().eqconv_block_norm_workspace_bytes(plan, int(N)))
+
+
+def eqconv_block_norm_backward(plan: int, N: int, x, b, gate, w_post, w_pre, scale: float, stats, g_x, g_h, dx, db,
+                               dgate, dw_post, dw_pre, workspace, workspace_bytes: int, stream=None) -> None:
+    _check(lib().eqconv_block_norm_backward(plan, N, x, b, gate, w_post, w_pre, scale, stats, g_x, g_h, dx, db, dgate,
+                                            dw_post, dw_pre, _ptr(workspace), workspace_bytes, _stream(stream)),
+           "eqconv_block_norm_backward")
+
+
+def eqconv_clip_workspace_bytes(n: int, tensors) -> int:
+    return int(lib().eqconv_clip_workspace_bytes(n, tensors))
+
+
+def eqconv_gradient_norm(n: int, tensors, norm, workspace, workspace_bytes: int, stream=None) -> None:
+    """tensors: an array of n eqconv_tensor_t, read during the call."""
+    _check(lib().eqconv_gradient_norm(n, tensors, _ptr(norm, _f32()), _ptr(workspace), workspace_bytes,
+                                      _stream(stream)), "eqconv_gradient_norm")
+
+
+def eqconv_clip_gradients(n: int, tensors, max_norm: float, eps: float, norm, workspace, workspace_bytes: int,
+                          stream=None) -> None:
+    _check(lib().eqconv_clip_gradients(n, tensors, max_norm, eps, _ptr(norm, _f32()), _ptr(workspace),
+                                       workspace_bytes, _stream(stream)), "eqconv_clip_gradients")
 
 
 def eqconv_spherical_harmonics(plan: int, E: int, r, Y, stream=None) -> None:

@@ -25,6 +25,7 @@
 #include "eqc_nodeprod.cuh"
 #include "eqc_dispatch.h"
 #include "eqc_graph.h"
+#include "eqc_plan.h"
 #include "eqc_radial.h"
 #include "eqc_radial_conv.h"
 #include "eqc_symc.cuh"
@@ -85,27 +86,6 @@ __global__ void k_zero_f4(float4* p, int64_t n4) {
 }
 
 }  // namespace eqc
-
-struct eqconv_plan_s {
-    int lin, lsh, lout, C;
-    int fwd_vec, det_vec, atomic_vec;
-    size_t gather_budget;   // bytes of gathered rows one band may touch (0: one band)
-    bool budget_set;        // false: per-mode defaults (bands for the atomic backward only)
-    int mode;               // output variant bits (eqc::kModeAllParity, eqc::kModePerPath)
-    int P, D_in, D_sh, D_out;
-    int paths[eqc::kMaxPaths][3];
-    int path_rows[eqc::kMaxPaths];
-    int device;
-    unsigned* d_status;
-    const eqc::KernelSet* fwd_ks;
-    const eqc::KernelSet* det_ks;      // deterministic backward
-    const eqc::KernelSet* atomic_ks;   // atomic backward
-    const eqc::DblKernelSet* dbl_ks;   // double backward (summed natural-parity outputs only)
-    bool node_product;                 // a node-local product plan (no convolution)
-    const eqc::NpKernelSet* np_ks;     // node-local product
-    const eqc::SymKernelSet* symc_ks;  // symmetric contraction (then node_product is true too)
-    int n_species;
-};
 
 namespace {
 
@@ -212,11 +192,8 @@ int bands_for(eqconv_plan_t plan, int N, int D, int tile_c, bool atomic_bwd) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-int check_device(eqconv_plan_t plan) {
-    int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess) return EQCONV_ERR_CUDA;
-    return dev == plan->device ? EQCONV_OK : EQCONV_ERR_INVALID_ARG;
-}
+using eqc::check_device;
+using eqc::cuda_status;
 
 int check_graph(const eqconv_graph_t* g) {
     if (!g || g->N < 0 || g->E < 0) return EQCONV_ERR_INVALID_ARG;
@@ -225,13 +202,25 @@ int check_graph(const eqconv_graph_t* g) {
     return EQCONV_OK;
 }
 
+}  // namespace
+
+namespace eqc {
+
+int check_device(eqconv_plan_t plan) {
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) return EQCONV_ERR_CUDA;
+    return dev == plan->device ? EQCONV_OK : EQCONV_ERR_INVALID_ARG;
+}
+
 int cuda_status(cudaError_t e, const char* where) {
     if (e == cudaSuccess) return EQCONV_OK;
-    eqc::note_error(where, e);
+    note_error(where, e);
     return EQCONV_ERR_CUDA;
 }
 
-}  // namespace
+int natural_prefix(const char* irreps) { return parse_natural_prefix(irreps); }
+
+}  // namespace eqc
 
 extern "C" {
 
@@ -910,6 +899,7 @@ void eqconv_plan_destroy(eqconv_plan_t plan) {
     if (switch_dev) cudaSetDevice(plan->device);
     cudaFree(plan->d_status);
     if (switch_dev) cudaSetDevice(cur);
+    delete plan->layer;
     delete plan;
 }
 

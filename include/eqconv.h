@@ -23,7 +23,9 @@
  * Besides the forward and the backward the library has the double backward
  * (eqconv_double_backward, the VJP of the backward, for training on forces)
  * and the node-local channel-diagonal product of two node features
- * (eqconv_node_product*, one step of the correlation ladder).
+ * (eqconv_node_product*, one step of the correlation ladder), and the
+ * node-level operators around a convolution (eqconv_embedding*,
+ * eqconv_block_norm*, eqconv_gradient_norm, eqconv_clip_gradients).
  *
  * Layout (FlashCart App. D, Figure D1: rank blocks, then components, then
  * channels): every tensor is fp32, row-major, channels innermost.
@@ -445,6 +447,116 @@ EQCONV_API int eqconv_backward_radial(eqconv_plan_t plan, const eqconv_graph_t* 
                                       const float* W1, const float* W2, const float* W3, int n_basis, float r_cut,
                                       const float* gy, float* dx, float* dr, float* gW1, float* gW2, float* gW3,
                                       void* workspace, size_t workspace_bytes, eqconv_stream_t stream);
+
+/* ---- Node-level operators around a convolution ----------------------------
+ * What a training step of a stack of convolutions does between them: the
+ * features a node starts from (type embedding), the norms, gate and residual
+ * around each layer (block norm), and the norm of all weight gradients with
+ * clipping.  Tensors are fp32, bf16 or fp16 (element type codes below), all
+ * arithmetic is fp32 or wider and each output is rounded once.  Pointers need
+ * the alignment of their elements only; rows on 16-byte boundaries are moved
+ * in 16-byte pieces. */
+enum { EQCONV_F32 = 0, EQCONV_BF16 = 1, EQCONV_F16 = 2 };
+
+/* Type embedding: y[i, :] = scale * T[ids[i], :] for N node (or token) types
+ * ids in 0..n_types-1, T [n_types][C].  1 <= C <= 65536, any n_types and
+ * N < 2^31 - 2.  out_type is the table's type, or a 16-bit type with an fp32
+ * table (EQCONV_ERR_UNSUPPORTED otherwise).  padding: the row of T that gets
+ * no gradient (-1: none; it is looked up like any other).  An embedding plan
+ * is not a convolution plan. */
+EQCONV_API int eqconv_embedding_plan_create(eqconv_plan_t* out, int64_t n_types, int C, int table_type, int out_type,
+                                            int64_t padding);
+
+/* y as above; one launch on `stream`.  ids are int32 or int64 (id_bits 32 or
+ * 64).  Rows of T and y start table_stride and y_stride elements apart (>= C).
+ * ids out of range set the status word (bit 1); their rows of y are 0. */
+EQCONV_API int eqconv_embedding(eqconv_plan_t plan, int64_t N, const void* ids, int id_bits, const void* table,
+                                int64_t table_stride, float scale, void* y, int64_t y_stride, eqconv_stream_t stream);
+
+/* Device workspace bytes eqconv_embedding_backward needs. */
+EQCONV_API size_t eqconv_embedding_workspace_bytes(eqconv_plan_t plan, int64_t N);
+
+/* dT [n_types][C] (the table's type, contiguous) given gy (out_type, rows
+ * gy_stride elements apart; 0 repeats one row):
+ *   dT[v, :] = scale * sum over nodes i with ids[i] = v of gy[i, :]
+ * 0 for the padding row and for types no node has; ids out of range set the
+ * status word and add nothing.  The nodes are ordered by type first (stable)
+ * and summed in fp32 in an order that depends on the sizes and ids alone:
+ * bitwise reproducible, no atomics on values.  All of dT is overwritten. */
+EQCONV_API int eqconv_embedding_backward(eqconv_plan_t plan, int64_t N, const void* ids, int id_bits, const void* gy,
+                                         int64_t gy_stride, float scale, void* dtable, void* workspace,
+                                         size_t workspace_bytes, eqconv_stream_t stream);
+
+/* Block norm: the root-mean-square norms before and after a layer, with the
+ * layer's gate and residual.  x, b [N][(L+1)^2][C] (irreps a natural-parity
+ * prefix; "0e" is the plain row norm over C), one mean per node and degree l
+ * (rms over its 2l+1 rows and C channels, which rotations leave unchanged):
+ *   u     = b / rms(b) * w_post[l, c]
+ *   x_out = x + scale * a(gate[n, l, c]) * u
+ *   h     = x_out / rms(x_out) * w_pre[l, c]          rms(v) = sqrt(mean(v^2) + eps)
+ * b is the layer's output, x the residual stream, h the next layer's input.
+ * w_post null (then b, gate and x_out are null too): x_out = x, the norm
+ * before a first layer.  w_pre null (then h is null): no next layer.
+ * gate [N][L+1][C] holds the gate's argument, a its function.
+ * x, b, gate, x_out, h have the plan's element type; w_post, w_pre [L+1][C]
+ * are fp32.  Squares are summed in fp32 (|v| up to about 1e18).
+ * 1 <= C <= 16384, eps > 0 and finite. */
+enum { EQCONV_GATE_NONE = 0, EQCONV_GATE_SIGMOID = 1, EQCONV_GATE_SILU = 2, EQCONV_GATE_TANH = 3 };
+
+EQCONV_API int eqconv_block_norm_plan_create(eqconv_plan_t* out, const char* irreps, int C, int type, int gate,
+                                             float eps);
+
+/* The forward; one launch on `stream`.  stats [2][N][L+1] fp32 receives
+ * 1 / rms(b) and 1 / rms(x_out) for the backward (null: not kept; the half of
+ * an absent norm is not written).  Outputs overlap no input. */
+EQCONV_API int eqconv_block_norm(eqconv_plan_t plan, int N, const void* x, const void* b, const void* gate,
+                                 const float* w_post, const float* w_pre, float scale, void* x_out, void* h,
+                                 float* stats, eqconv_stream_t stream);
+
+/* Device workspace bytes eqconv_block_norm_backward needs (partial sums of
+ * the weight gradients). */
+EQCONV_API size_t eqconv_block_norm_workspace_bytes(eqconv_plan_t plan, int N);
+
+/* Backward given g_x and g_h, the gradients of x_out and h (null: zero):
+ * dx, db, dgate (element type of the plan; dgate null without a gate) and
+ * dw_post, dw_pre [L+1][C] fp32 (either may be null: not computed).  x_out is
+ * formed again from x, b and gate; stats are the forward's.  The weight
+ * gradients are summed in a fixed order: bitwise reproducible.  Outputs
+ * overlap no input and are overwritten. */
+EQCONV_API int eqconv_block_norm_backward(eqconv_plan_t plan, int N, const void* x, const void* b, const void* gate,
+                                          const float* w_post, const float* w_pre, float scale, const float* stats,
+                                          const void* g_x, const void* g_h, void* dx, void* db, void* dgate,
+                                          float* dw_post, float* dw_pre, void* workspace, size_t workspace_bytes,
+                                          eqconv_stream_t stream);
+
+/* One tensor of a list: n elements at `in` (contiguous), of a type code; the
+ * scaled elements go to `out` (which may be `in`). */
+typedef struct eqconv_tensor_s {
+    const void* in;
+    void* out;
+    int64_t n;
+    int32_t type;
+    int32_t reserved;
+} eqconv_tensor_t;
+
+/* Device workspace bytes that the two calls below need for this list (0 for
+ * a list they refuse). */
+EQCONV_API size_t eqconv_clip_workspace_bytes(int n, const eqconv_tensor_t* tensors);
+
+/* *norm (device, fp32) = sqrt(sum over the list of all elements squared).
+ * The list is read on the host during the call; `out` is not used.  Squares
+ * are summed in fp64 in a fixed order.  These calls take no plan: the list
+ * and the workspace live on the current device. */
+EQCONV_API int eqconv_gradient_norm(int n, const eqconv_tensor_t* tensors, float* norm, void* workspace,
+                                    size_t workspace_bytes, eqconv_stream_t stream);
+
+/* The norm as above, and out = k * in with k = min(1, max_norm / (norm + eps))
+ * for every tensor.  In place, nothing is written when k = 1.  A norm that is
+ * infinite gives k = 0, one that is NaN gives NaN everywhere.  max_norm >= 0,
+ * eps > 0.  An output that overlaps another tensor of the list, or its own
+ * input without being it, is refused (EQCONV_ERR_INVALID_ARG). */
+EQCONV_API int eqconv_clip_gradients(int n, const eqconv_tensor_t* tensors, float max_norm, float eps, float* norm,
+                                     void* workspace, size_t workspace_bytes, eqconv_stream_t stream);
 
 /* The spherical harmonics the kernels use, Y [E][(L_sh+1)^2] (a test hook
  * for the in-kernel harmonics; not on the hot path). */

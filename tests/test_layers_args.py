@@ -1,0 +1,126 @@
+"""The node-level operators' checks of their arguments, without a GPU: every
+refusal below comes before any device work."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from equivariant_gnn_message_edge_b200 import binding as B
+from equivariant_gnn_message_edge_b200 import layers
+
+
+@pytest.mark.parametrize("args,status", [
+    ((0, 8, 0, 0, -1), B.EQCONV_ERR_INVALID_ARG),           # no types
+    ((8, 0, 0, 0, -1), B.EQCONV_ERR_INVALID_ARG),           # no channels
+    ((8, 8, 3, 3, -1), B.EQCONV_ERR_INVALID_ARG),           # unknown element type
+    ((8, 8, 0, 0, 8), B.EQCONV_ERR_INVALID_ARG),            # padding is no type
+    ((8, 8, 0, 0, -2), B.EQCONV_ERR_INVALID_ARG),
+    ((8, 8, 1, 0, -1), B.EQCONV_ERR_UNSUPPORTED),           # bf16 table, fp32 rows
+    ((8, 8, 1, 2, -1), B.EQCONV_ERR_UNSUPPORTED),           # bf16 table, fp16 rows
+    ((8, 65537, 0, 0, -1), B.EQCONV_ERR_UNSUPPORTED),       # too wide
+    ((2 ** 31 - 1, 8, 0, 0, -1), B.EQCONV_ERR_UNSUPPORTED)])
+def test_embedding_plans_validate(args, status):
+    with pytest.raises(B.EqconvError) as e:
+        B.eqconv_embedding_plan_create(*args)
+    assert e.value.status == status
+
+
+@pytest.mark.parametrize("args,status", [
+    (("0e+1q", 8, 0, 1, 1e-6), B.EQCONV_ERR_INVALID_ARG),
+    (("0e+2e", 8, 0, 1, 1e-6), B.EQCONV_ERR_UNSUPPORTED),
+    (("0e", 0, 0, 1, 1e-6), B.EQCONV_ERR_INVALID_ARG),
+    (("0e", 16385, 0, 1, 1e-6), B.EQCONV_ERR_UNSUPPORTED),
+    (("0e", 8, 5, 1, 1e-6), B.EQCONV_ERR_INVALID_ARG),
+    (("0e", 8, 0, 4, 1e-6), B.EQCONV_ERR_INVALID_ARG),
+    (("0e", 8, 0, 1, 0.0), B.EQCONV_ERR_INVALID_ARG),
+    (("0e", 8, 0, 1, float("nan")), B.EQCONV_ERR_INVALID_ARG),
+    (("0e", 8, 0, 1, float("inf")), B.EQCONV_ERR_INVALID_ARG)])
+def test_block_norm_plans_validate(args, status):
+    with pytest.raises(B.EqconvError) as e:
+        B.eqconv_block_norm_plan_create(*args)
+    assert e.value.status == status
+
+
+def test_null_and_foreign_plans_are_refused():
+    assert B.eqconv_embedding_workspace_bytes(0, 10) == 0
+    assert B.eqconv_block_norm_workspace_bytes(0, 10) == 0
+    with pytest.raises(B.EqconvError) as e:
+        B.eqconv_embedding(None, 1, 16, 32, 16, 8, 1.0, 16, 8, 0)
+    assert e.value.status == B.EQCONV_ERR_INVALID_ARG
+    with pytest.raises(B.EqconvError) as e:
+        B.eqconv_block_norm(None, 1, 16, None, None, None, 16, 1.0, None, 16, None, 0)
+    assert e.value.status == B.EQCONV_ERR_INVALID_ARG
+
+
+def _list(*rows):
+    return (B.eqconv_tensor_t * max(1, len(rows)))(*[B.eqconv_tensor_t(*r, 0) for r in rows]), len(rows)
+
+
+# host addresses stand in for device memory: the refusals below never read them
+BASE = 1 << 20
+
+
+@pytest.mark.parametrize("rows", [
+    [(BASE, BASE, -1, 0)],                                            # negative length
+    [(BASE, BASE, 4, 3)],                                             # unknown type
+    [(None, BASE, 4, 0)],                                             # no input
+    [(BASE, None, 4, 0)],                                             # no output
+    [(BASE + 2, BASE + 2, 4, 0)],                                     # half an element off
+    [(BASE, BASE, 8, 0), (BASE, BASE, 8, 0)],                         # the same tensor twice
+    [(BASE, BASE, 8, 0), (BASE + 16, BASE + 16, 8, 0)],               # neighbours that overlap
+    [(BASE, BASE + 16, 8, 0)],                                        # an output inside its own input
+    [(BASE, BASE + 4096, 8, 0), (BASE + 64, BASE + 4100, 8, 0)],      # two outputs overlap
+    [(BASE, BASE + 64, 8, 0), (BASE + 64, BASE + 128, 8, 0)],         # an output is another's input
+])
+def test_clip_refuses(rows):
+    arr, n = _list(*rows)
+    with pytest.raises(B.EqconvError) as e:
+        B.eqconv_clip_gradients(n, arr, 1.0, 1e-6, BASE * 4, BASE * 8, 1 << 30, 0)
+    assert e.value.status == B.EQCONV_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("max_norm,eps", [(-1.0, 1e-6), (float("nan"), 1e-6), (1.0, 0.0), (1.0, -1.0),
+                                          (1.0, float("inf")), (1.0, float("nan"))])
+def test_clip_refuses_bounds(max_norm, eps):
+    arr, n = _list((BASE, BASE, 8, 0))
+    with pytest.raises(B.EqconvError) as e:
+        B.eqconv_clip_gradients(n, arr, max_norm, eps, BASE * 4, BASE * 8, 1 << 30, 0)
+    assert e.value.status == B.EQCONV_ERR_INVALID_ARG
+
+
+def test_clip_workspace():
+    arr, n = _list((BASE, BASE, 1 << 20, 0), (BASE * 64, BASE * 64, 5, 1))
+    need = B.eqconv_clip_workspace_bytes(n, arr)
+    assert need > 0
+    for ws, size in ((None, need), (BASE * 8, need - 1), (BASE * 8 + 8, need)):
+        with pytest.raises(B.EqconvError) as e:
+            B.eqconv_clip_gradients(n, arr, 1.0, 1e-6, BASE * 4, ws, size, 0)
+        assert e.value.status == B.EQCONV_ERR_WORKSPACE
+        with pytest.raises(B.EqconvError) as e:
+            B.eqconv_gradient_norm(n, arr, BASE * 4, ws, size, 0)
+        assert e.value.status == B.EQCONV_ERR_WORKSPACE
+    bad, m = _list((BASE, BASE, -1, 0))
+    assert B.eqconv_clip_workspace_bytes(m, bad) == 0
+
+
+def test_python_refusals():
+    with pytest.raises(TypeError):
+        layers.clip_gradients(torch.zeros(3), 1.0)
+    with pytest.raises(ValueError):
+        layers.clip_gradients([torch.zeros(3)], 1.0)             # not on a GPU
+    with pytest.raises(TypeError):
+        layers.gradient_norm([np.zeros(3)])
+    with pytest.raises(ValueError):
+        layers.BlockNorm("0e", 8, gate="relu")
+    with pytest.raises(ValueError):
+        layers.BlockNorm("0e", 8, dtype=torch.float64)
+    with pytest.raises(ValueError):
+        layers.Embedding(4, 8, dtype=torch.float64)
+    with pytest.raises(ValueError):
+        layers.Embedding(4, 8, padding=4)
+
+
+def test_tensor_record_layout():
+    assert ctypes.sizeof(B.eqconv_tensor_t) == 32
+    assert [getattr(B.eqconv_tensor_t, f).offset for f in ("in_", "out", "n", "type")] == [0, 8, 16, 24]
