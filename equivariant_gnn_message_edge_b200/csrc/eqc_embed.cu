@@ -1,12 +1,15 @@
 // Type embedding: rows of a table gathered and scaled, and the gradient of the
 // table summed over the nodes of each type in node order.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "eqc_elem.cuh"
-#include "eqc_graph.h"
 #include "eqc_layers.h"
+
+namespace cg = cooperative_groups;
 
 namespace eqc {
 
@@ -59,38 +62,396 @@ __global__ void __launch_bounds__(256) embed_fwd_kernel(const void* ids, int64_t
     }
 }
 
-// int32 sort keys: the id, or V for ids that give no gradient.
+// ---------------------------------------------------------------------------
+// Gradient of the table.  The nodes are ordered by type (stable), and tiles of
+// R ordered nodes are summed in that order.  A type whose nodes lie inside one
+// tile is finished there; a type that reaches over tile ends leaves one partial
+// row per tile, which a second kernel adds in tile order.  Ids that give no
+// gradient (padding, out of range) get the key V and come last.
+
 template <class ID>
-__global__ void embed_keys_kernel(const void* ids, int64_t N, int64_t V, int64_t padding, int* keys,
-                                  unsigned* status) {
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= N) return;
+__device__ __forceinline__ int key_of(const void* ids, int64_t i, int64_t V, int64_t padding, unsigned* status) {
     const int64_t id = id_at<ID>(ids, i);
     const bool ok = (uint64_t)id < (uint64_t)V;
     if (!ok) atomicOr(status, 1u);
-    keys[i] = ok && id != padding ? (int)id : (int)V;
+    return ok && id != padding ? (int)id : (int)V;
 }
 
-// dT[v, :] = scale * sum over the type's nodes, in node order.
+constexpr int kDigitBits = 9;                 // radix of one sorting pass: at most 512
+constexpr int kRadix = 1 << kDigitBits;
+
+// Ranks a warp's 32 keys of one round by digit, stably, behind the keys that
+// the warp ranked in earlier rounds (counted in h[digit]).
+__device__ __forceinline__ int warp_rank(int* h, int d, bool valid) {
+    const int lane = threadIdx.x & 31;
+    const unsigned peers = __match_any_sync(0xffffffffu, valid ? d : kRadix + lane);
+    const int before = __popc(peers & ((1u << lane) - 1u));
+    const int rank = valid ? h[d] + before : 0;
+    __syncwarp();
+    if (valid && before == 0) h[d] += __popc(peers);
+    __syncwarp();
+    return rank;
+}
+
+// Sum of v over the lower-ranked threads of the block (THREADS of them).
+template <int THREADS>
+__device__ __forceinline__ int block_exclusive(int v, int* warp_sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+    }
+    if (lane == 31) warp_sums[warp] = inc;
+    __syncthreads();
+    int off = 0;
+    for (int w = 0; w < warp; ++w) off += warp_sums[w];
+    return off + inc - v;
+}
+
+// Sort of up to 8 x 8192 nodes in one launch by one cluster: keys and node
+// numbers stay in the CTAs' shared memory between passes and are scattered
+// into each other's over the cluster (least significant digit first).  Bound
+// by latency; the launch it saves per step is worth more than its idle SMs.
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortRounds = 8;
+constexpr int kSortCap = kSortThreads * kSortRounds;
+constexpr int kMaxCluster = 8;
+
+struct SortSmem {
+    int key[2][kSortCap];
+    int idx[2][kSortCap];
+    int hist[kSortWarps][kRadix];
+    int total[kRadix];
+    int base[kRadix];
+    int warp_sums[kSortWarps];
+};
+
+template <class ID>
+__global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const void* ids, int N, int64_t V, int64_t padding,
+                                                                  int rounds_log2, int digit_bits, int passes,
+                                                                  int* keys, int* perm, unsigned* status) {
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    SortSmem& s = *reinterpret_cast<SortSmem*>(smem_raw);
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rounds = 1 << rounds_log2, cap_log2 = 10 + rounds_log2, cap = 1 << cap_log2;
+    const int radix = 1 << digit_bits;
+    const int first = warp * 32 * rounds + lane;       // this thread's items: first + 32 k
+    for (int k = 0; k < rounds; ++k) {
+        const int j = first + 32 * k, i = rank * cap + j;
+        if (i < N) {
+            s.key[0][j] = key_of<ID>(ids, i, V, padding, status);
+            s.idx[0][j] = i;
+        }
+    }
+    for (int p = 0; p < passes; ++p) {
+        const int shift = p * digit_bits, cur = p & 1;
+        int key[kSortRounds], at[kSortRounds];
+        for (int d = lane; d < radix; d += 32) s.hist[warp][d] = 0;
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < kSortRounds; ++k) {
+            if (k >= rounds) break;
+            const int j = first + 32 * k;
+            const bool valid = rank * cap + j < N;
+            key[k] = valid ? s.key[cur][j] : 0;
+            at[k] = warp_rank(s.hist[warp], (key[k] >> shift) & (radix - 1), valid);
+        }
+        __syncthreads();
+        if (tid < radix) {
+            int run = 0;
+#pragma unroll 8
+            for (int w = 0; w < kSortWarps; ++w) {
+                const int c = s.hist[w][tid];
+                s.hist[w][tid] = run;
+                run += c;
+            }
+            s.total[tid] = run;
+        }
+        cluster.sync();
+        int all = 0, below = 0;
+        if (tid < radix)
+            for (int q = 0; q < ctas; ++q) {
+                const int c = *cluster.map_shared_rank(&s.total[tid], q);
+                all += c;
+                if (q < rank) below += c;
+            }
+        const int excl = block_exclusive<kSortThreads>(all, s.warp_sums);
+        if (tid < radix) s.base[tid] = excl + below;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kSortRounds; ++k) {
+            if (k >= rounds) break;
+            const int j = first + 32 * k;
+            if (rank * cap + j >= N) continue;
+            const int d = (key[k] >> shift) & (radix - 1);
+            const int pos = s.base[d] + s.hist[warp][d] + at[k], idx = s.idx[cur][j];
+            if (p == passes - 1) {
+                keys[pos] = key[k];
+                perm[pos] = idx;
+            } else {
+                const int q = pos >> cap_log2, o = pos & (cap - 1);
+                *cluster.map_shared_rank(&s.key[cur ^ 1][o], q) = key[k];
+                *cluster.map_shared_rank(&s.idx[cur ^ 1][o], q) = idx;
+            }
+        }
+        cluster.sync();
+    }
+}
+
+// Sort of more nodes: per pass a histogram of every tile of 4096 nodes, a scan
+// over the tiles by digit, and a stable scatter.
+constexpr int kLsdThreads = 512;
+constexpr int kLsdRounds = 8;
+constexpr int kLsdTile = kLsdThreads * kLsdRounds;
+static_assert(kLsdThreads == kRadix, "one thread per digit");
+
+// The key of node i of a pass: from the ids (first pass), or from the last pass.
+template <class ID, bool FIRST>
+__device__ __forceinline__ int pass_key(const void* in, int64_t i, int64_t V, int64_t padding, unsigned* status) {
+    if constexpr (FIRST) return key_of<ID>(in, i, V, padding, status);
+    else return static_cast<const int*>(in)[i];
+}
+
+template <class ID, bool FIRST>
+__global__ void __launch_bounds__(kLsdThreads) embed_hist_kernel(const void* in, int N, int64_t V, int64_t padding,
+                                                                 int shift, int mask, int* hist, int tiles,
+                                                                 unsigned* status) {
+    __shared__ int h[kRadix];
+    h[threadIdx.x] = 0;
+    __syncthreads();
+    const int64_t i0 = (int64_t)blockIdx.x * kLsdTile + threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < kLsdRounds; ++k) {
+        const int64_t i = i0 + k * kLsdThreads;
+        const bool valid = i < N;
+        const int d = valid ? (pass_key<ID, FIRST>(in, i, V, padding, status) >> shift) & mask : 0;
+        // lanes with one digit count it once: a table of few types would serialise on it
+        const unsigned peers = __match_any_sync(0xffffffffu, valid ? d : kRadix + (threadIdx.x & 31));
+        if (valid && __ffs(peers) - 1 == (int)(threadIdx.x & 31)) atomicAdd(&h[d], __popc(peers));
+    }
+    __syncthreads();
+    if ((int)threadIdx.x <= mask) hist[(int64_t)threadIdx.x * tiles + blockIdx.x] = h[threadIdx.x];
+}
+
+// hist[d][*] becomes its exclusive scan over the tiles, total[d] its sum: one warp per digit.
+__global__ void embed_scan_kernel(int* hist, int tiles, int radix, int* total) {
+    const int d = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
+    if (d >= radix) return;
+    int* h = hist + (int64_t)d * tiles;
+    int run = 0;
+    for (int t = 0; t < tiles; t += 32) {
+        const int v = t + lane < tiles ? h[t + lane] : 0;
+        int inc = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += u;
+        }
+        if (t + lane < tiles) h[t + lane] = run + inc - v;
+        run += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (lane == 0) total[d] = run;
+}
+
+template <class ID, bool FIRST>
+__global__ void __launch_bounds__(kLsdThreads) embed_scatter_kernel(const void* in, const int* idx_in, int N,
+                                                                    int64_t V, int64_t padding, int shift, int mask,
+                                                                    const int* hist, const int* total, int tiles,
+                                                                    int* keys_out, int* idx_out, unsigned* status) {
+    __shared__ int wh[kLsdThreads / 32][kRadix];
+    __shared__ int base[kRadix];
+    __shared__ int sums[kLsdThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int d = lane; d <= mask; d += 32) wh[warp][d] = 0;
+    const int excl = block_exclusive<kLsdThreads>(tid <= mask ? total[tid] : 0, sums);
+    if (tid <= mask) base[tid] = excl + hist[(int64_t)tid * tiles + blockIdx.x];
+    __syncwarp();
+    const int64_t i0 = (int64_t)blockIdx.x * kLsdTile + warp * 32 * kLsdRounds + lane;
+    int key[kLsdRounds], at[kLsdRounds];
+#pragma unroll
+    for (int k = 0; k < kLsdRounds; ++k) {
+        const bool valid = i0 + 32 * k < N;
+        key[k] = valid ? pass_key<ID, FIRST>(in, i0 + 32 * k, V, padding, status) : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kLsdRounds; ++k) at[k] = warp_rank(wh[warp], (key[k] >> shift) & mask, i0 + 32 * k < N);
+    __syncthreads();
+    if (tid <= mask) {
+        int run = base[tid];
+#pragma unroll
+        for (int w = 0; w < kLsdThreads / 32; ++w) {
+            const int c = wh[w][tid];
+            wh[w][tid] = run;
+            run += c;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kLsdRounds; ++k) {
+        const int64_t i = i0 + 32 * k;
+        if (i >= N) continue;
+        const int pos = wh[warp][(key[k] >> shift) & mask] + at[k];
+        keys_out[pos] = key[k];
+        idx_out[pos] = FIRST ? (int)i : idx_in[i];
+    }
+}
+
+struct SumParams {
+    const int *keys, *perm;   // nodes in type order
+    int N, C, R, tiles, slabs, lx_log2;
+    int sum_blocks, zero_rows;
+    int64_t V, ldg;
+    float scale;
+    float* part;              // [tiles][2][C]: the type begun before the tile, the one that goes on behind it
+};
+
+// First position whose key is not below k.
+__device__ __forceinline__ int lower_bound(const int* keys, int n, int k) {
+    int lo = 0, hi = n;
+    while (lo < hi) {
+        const int mid = (int)(((unsigned)lo + (unsigned)hi) >> 1);
+        if (__ldg(keys + mid) < k) lo = mid + 1;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// Blocks up to sum_blocks: one worker (1 << lx_log2 lanes) per tile and slab of
+// channels; the rest write zeros to the rows of types without nodes, which the
+// ordered keys show by search.  Bound by memory: gy is read once, dT written once.
 template <class T, class O, int VE>
-__global__ void embed_bwd_kernel(const int* ptr, const int* perm, int64_t V, int C, const O* gy, int64_t ldg,
-                                 float scale, T* dtable) {
-    const int c = (blockIdx.y * 32 + threadIdx.x) * VE;
-    const int64_t v = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    if (v >= V || c >= C) return;
+__global__ void __launch_bounds__(256) embed_sum_kernel(const SumParams p, const O* gy, T* dtable) {
+    if ((int)blockIdx.x >= p.sum_blocks) {
+        __shared__ bool empty[256];
+        const int64_t v0 = (int64_t)(blockIdx.x - p.sum_blocks) * p.zero_rows;
+        const int rows = (int)(p.V - v0 < p.zero_rows ? p.V - v0 : p.zero_rows);
+        if ((int)threadIdx.x < rows) {
+            const int v = (int)(v0 + threadIdx.x), at = lower_bound(p.keys, p.N, v);
+            empty[threadIdx.x] = at >= p.N || p.keys[at] != v;
+        }
+        __syncthreads();
+        Pack<T, VE> zero;
+#pragma unroll
+        for (int e = 0; e < VE; ++e) zero.set(e, 0.f);
+        const int vecs = p.C / VE;
+        for (int r = 0, c = threadIdx.x;; c += 256) {
+            while (c >= vecs) {
+                c -= vecs;
+                ++r;
+            }
+            if (r >= rows) break;
+            if (empty[r]) zero.store(dtable + (v0 + r) * p.C + (int64_t)c * VE);
+        }
+        return;
+    }
+    const int64_t worker = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> p.lx_log2;
+    const int tile = (int)(worker / p.slabs), slab = (int)(worker % p.slabs);
+    const int c = ((slab << p.lx_log2) + (threadIdx.x & ((1 << p.lx_log2) - 1))) * VE;
+    if (tile >= p.tiles || c >= p.C) return;
+    const int64_t q0 = (int64_t)tile * p.R;
+    const int n = (int)(p.N - q0 < p.R ? p.N - q0 : p.R);
+    const int *keys = p.keys + q0, *perm = p.perm + q0;
+    const int none = (int)p.V;
+    int cur = __ldg(keys);
+    bool begun_before = tile > 0 && __ldg(keys - 1) == cur;
     float acc[VE];
 #pragma unroll
     for (int e = 0; e < VE; ++e) acc[e] = 0.f;
-    for (int p = ptr[v]; p < ptr[v + 1]; ++p) {
-        Pack<O, VE> in;
-        in.load(gy + (int64_t)perm[p] * ldg + c);
+    float* part = p.part + (int64_t)tile * 2 * p.C + c;
+    const auto row = [&](int v) {
+        Pack<T, VE> out;
 #pragma unroll
-        for (int e = 0; e < VE; ++e) acc[e] += in.get(e);
+        for (int e = 0; e < VE; ++e) out.set(e, acc[e] * p.scale);
+        out.store(dtable + (int64_t)v * p.C + c);
+    };
+    const auto partial = [&](int which) {
+        Pack<float, VE> out;
+#pragma unroll
+        for (int e = 0; e < VE; ++e) out.e[e] = acc[e];
+        out.store(part + which * p.C);
+    };
+    constexpr int kAhead = 8;
+    for (int j0 = 0; j0 < n; j0 += kAhead) {
+        Pack<O, VE> in[kAhead];
+        int key[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            key[u] = j0 + u < n ? __ldg(keys + j0 + u) : none;
+            if (key[u] != none) in[u].load(gy + (int64_t)__ldg(perm + j0 + u) * p.ldg + c);
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (j0 + u >= n) break;
+            if (key[u] != cur) {
+                if (begun_before) partial(0);
+                else row(cur);
+                begun_before = false;
+                cur = key[u];
+#pragma unroll
+                for (int e = 0; e < VE; ++e) acc[e] = 0.f;
+            }
+            if (cur == none) break;
+#pragma unroll
+            for (int e = 0; e < VE; ++e) acc[e] += in[u].get(e);
+        }
+        if (cur == none) return;
     }
+    if (begun_before) partial(0);
+    else if (q0 + n < p.N && __ldg(keys + n) == cur) partial(1);
+    else row(cur);
+}
+
+// Types that reach over tile ends: the tile in which such a type begins adds
+// its partial row and those of the tiles behind it, shares of them by worker
+// and the workers' sums in order.
+template <class T, int VE>
+__global__ void __launch_bounds__(256) embed_join_kernel(const SumParams p, T* dtable) {
+    const int tile = blockIdx.x, slab = blockIdx.y;
+    const int64_t end = (int64_t)(tile + 1) * p.R;       // < N for every tile of the grid
+    const int k = __ldg(p.keys + end - 1);
+    if (k == (int)p.V || __ldg(p.keys + end) != k) return;
+    if (tile > 0 && __ldg(p.keys + end - p.R - 1) == k) return;      // begun in an earlier tile
+    const int last = (lower_bound(p.keys, p.N, k + 1) - 1) / p.R;     // tile of the type's last node
+    const int lanes = 1 << p.lx_log2, workers = 256 >> p.lx_log2;
+    const int x = threadIdx.x & (lanes - 1), w = threadIdx.x >> p.lx_log2;
+    const int c = ((slab << p.lx_log2) + x) * VE;
+    const int share = (last - tile + workers - 1) / workers;          // of the tiles behind the first
+    const int t0 = tile + 1 + w * share, t1 = t0 + share < last + 1 ? t0 + share : last + 1;
+    __shared__ float sums[256 * VE];
+    float acc[VE];
+#pragma unroll
+    for (int e = 0; e < VE; ++e) acc[e] = 0.f;
+    if (c < p.C) {
+        if (w == 0) {
+            Pack<float, VE> v;
+            v.load(p.part + ((int64_t)tile * 2 + 1) * p.C + c);
+#pragma unroll
+            for (int e = 0; e < VE; ++e) acc[e] = v.e[e];
+        }
+#pragma unroll 4
+        for (int t = t0; t < t1; ++t) {
+            Pack<float, VE> v;
+            v.load(p.part + (int64_t)t * 2 * p.C + c);
+#pragma unroll
+            for (int e = 0; e < VE; ++e) acc[e] += v.e[e];
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < VE; ++e) sums[threadIdx.x * VE + e] = acc[e];
+    __syncthreads();
+    if (w != 0 || c >= p.C) return;
+    for (int o = 1; o < workers; ++o)
+#pragma unroll
+        for (int e = 0; e < VE; ++e) acc[e] += sums[((o << p.lx_log2) + x) * VE + e];
     Pack<T, VE> out;
 #pragma unroll
-    for (int e = 0; e < VE; ++e) out.set(e, acc[e] * scale);
-    out.store(dtable + v * C + c);
+    for (int e = 0; e < VE; ++e) out.set(e, acc[e] * p.scale);
+    out.store(dtable + (int64_t)k * p.C + c);
 }
 
 // Calls f with the largest of 8 (16-bit outputs), 4, 2 and 1 elements a vector
@@ -143,41 +504,148 @@ cudaError_t embed_forward(const EmbedArgs& a, const void* table, int64_t table_s
 }
 
 namespace {
-struct EmbedWs {
-    size_t keys, ptr, perm, sort, total;
+
+// How the sum is cut for (N, C): slabs of 32 vectors (or one slab of fewer
+// lanes), and tiles of R nodes so that about 32 workers run on every SM, with
+// whole batches of 8 rows in flight.
+struct SumShape {
+    int ve, lx_log2, slabs, R, tiles;
 };
-EmbedWs embed_layout(int64_t V, int64_t N) {
+SumShape sum_shape(int64_t N, int C, int ve) {
+    SumShape s{};
+    s.ve = ve;
+    const int vecs = C / ve;
+    while (s.lx_log2 < 5 && (1 << s.lx_log2) < vecs) ++s.lx_log2;
+    s.slabs = cdiv(vecs, 1 << s.lx_log2);
+    const int64_t lanes = N * s.slabs << s.lx_log2;
+    int64_t R = (lanes / (148 * 1024) + 7) / 8 * 8;
+    s.R = (int)(R < 8 ? 8 : R > 256 ? 256 : R);
+    s.tiles = cdiv(N, s.R);
+    return s;
+}
+
+int bit_length(int64_t v) {
+    int b = 0;
+    for (; v; v >>= 1) ++b;
+    return b;
+}
+
+struct EmbedWs {
+    size_t keys, perm, keys2, perm2, hist, total, part, bytes;
+};
+// Space for any of the vector widths (the widest tiles come with width 1).
+EmbedWs embed_layout(int C, int64_t N) {
     const auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
     EmbedWs w{};
     size_t o = 0;
     w.keys = o; o += up(4 * (size_t)N);
-    w.ptr = o;  o += up(4 * (size_t)(V + 2));
     w.perm = o; o += up(4 * (size_t)N);
-    w.sort = o; o += csr_workspace_bytes((int)(V + 1), (int)N);
-    w.total = o;
+    if (N > (int64_t)kMaxCluster * kSortCap) {
+        const size_t tiles = cdiv(N, kLsdTile);
+        w.keys2 = o; o += up(4 * (size_t)N);
+        w.perm2 = o; o += up(4 * (size_t)N);
+        w.hist = o;  o += up(4 * tiles * kRadix);
+        w.total = o; o += up(4 * kRadix);
+    }
+    size_t tiles = 0;
+    for (const int ve : {1, 2, 4, 8}) {
+        if (C % ve) continue;
+        const size_t t = sum_shape(N, C, ve).tiles;
+        if (t > tiles) tiles = t;
+    }
+    w.part = o; o += up(tiles * 2 * C * sizeof(float));
+    w.bytes = o > 0 ? o : 16;
     return w;
 }
+
+template <class ID>
+cudaError_t sort_in_cluster(const EmbedArgs& a, int digit_bits, int passes, int* keys, int* perm, cudaStream_t st) {
+    // one CTA up to 4096 nodes, then clusters of 2, 4 and 8
+    int ctas = 1, rounds_log2 = 0;
+    while (ctas < kMaxCluster && a.N > (int64_t)ctas * 4096) ctas *= 2;
+    while (((int64_t)ctas * kSortThreads << rounds_log2) < a.N) ++rounds_log2;
+    static bool done[64] = {};
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 0 || dev >= 64 || !done[dev]) {
+        err = cudaFuncSetAttribute(embed_sort_kernel<ID>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   (int)sizeof(SortSmem));
+        if (err != cudaSuccess) return err;
+        if (dev >= 0 && dev < 64) done[dev] = true;
+    }
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = ctas;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = sizeof(SortSmem);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    err = cudaLaunchKernelEx(&cfg, embed_sort_kernel<ID>, a.ids, (int)a.N, a.V, a.padding, rounds_log2, digit_bits,
+                             passes, keys, perm, a.status);
+    count_launch();
+    return err;
+}
+
+template <class ID>
+cudaError_t sort_in_tiles(const EmbedArgs& a, int digit_bits, int passes, char* base, const EmbedWs& w, int** keys,
+                          int** perm, cudaStream_t st) {
+    int* k[2] = {reinterpret_cast<int*>(base + w.keys), reinterpret_cast<int*>(base + w.keys2)};
+    int* x[2] = {reinterpret_cast<int*>(base + w.perm), reinterpret_cast<int*>(base + w.perm2)};
+    int* hist = reinterpret_cast<int*>(base + w.hist);
+    int* total = reinterpret_cast<int*>(base + w.total);
+    const int tiles = cdiv(a.N, kLsdTile), radix = 1 << digit_bits, N = (int)a.N;
+    for (int p = 0; p < passes; ++p) {
+        const int shift = p * digit_bits, o = p & 1;
+        if (p == 0)
+            embed_hist_kernel<ID, true><<<tiles, kLsdThreads, 0, st>>>(a.ids, N, a.V, a.padding, shift, radix - 1,
+                                                                       hist, tiles, a.status);
+        else
+            embed_hist_kernel<ID, false><<<tiles, kLsdThreads, 0, st>>>(k[o ^ 1], N, a.V, a.padding, shift, radix - 1,
+                                                                        hist, tiles, a.status);
+        embed_scan_kernel<<<cdiv(radix, 8), 256, 0, st>>>(hist, tiles, radix, total);
+        if (p == 0)
+            embed_scatter_kernel<ID, true><<<tiles, kLsdThreads, 0, st>>>(a.ids, nullptr, N, a.V, a.padding, shift,
+                                                                          radix - 1, hist, total, tiles, k[o], x[o],
+                                                                          a.status);
+        else
+            embed_scatter_kernel<ID, false><<<tiles, kLsdThreads, 0, st>>>(k[o ^ 1], x[o ^ 1], N, a.V, a.padding,
+                                                                           shift, radix - 1, hist, total, tiles, k[o],
+                                                                           x[o], a.status);
+        for (int i = 0; i < 3; ++i) count_launch();
+        const cudaError_t err = cudaGetLastError();
+        if (err != cudaSuccess) return err;
+        *keys = k[o];
+        *perm = x[o];
+    }
+    return cudaSuccess;
+}
+
 }  // namespace
 
-size_t embed_workspace(int64_t V, int, int64_t N) { return embed_layout(V, N).total; }
+size_t embed_workspace(int64_t, int C, int64_t N) { return embed_layout(C, N).bytes; }
 
 cudaError_t embed_backward(const EmbedArgs& a, const void* gy, int64_t gy_stride, void* dtable, void* ws,
                            cudaStream_t st) {
-    const EmbedWs w = embed_layout(a.V, a.N);
+    if (a.N == 0)
+        return cudaMemsetAsync(dtable, 0, (size_t)a.V * a.C * type_bytes(a.in_type), st);
+    const EmbedWs w = embed_layout(a.C, a.N);
     char* base = static_cast<char*>(ws);
     int* keys = reinterpret_cast<int*>(base + w.keys);
-    int* ptr = reinterpret_cast<int*>(base + w.ptr);
     int* perm = reinterpret_cast<int*>(base + w.perm);
-    if (a.N > 0) {
-        if (a.id_bits == 32)
-            embed_keys_kernel<int32_t><<<cdiv(a.N, 256), 256, 0, st>>>(a.ids, a.N, a.V, a.padding, keys, a.status);
-        else
-            embed_keys_kernel<int64_t><<<cdiv(a.N, 256), 256, 0, st>>>(a.ids, a.N, a.V, a.padding, keys, a.status);
-        count_launch();
-    }
-    cudaError_t err = cudaGetLastError();
-    if (err != cudaSuccess) return err;
-    err = csr_build(keys, (int)(a.V + 1), (int)a.N, ptr, perm, base + w.sort, a.status, st);
+    // keys 0..V in equal digits of at most 9 bits
+    const int bits = bit_length(a.V), passes = cdiv(bits, kDigitBits), digit_bits = cdiv(bits, passes);
+    cudaError_t err;
+    if (a.N <= (int64_t)kMaxCluster * kSortCap)
+        err = a.id_bits == 32 ? sort_in_cluster<int32_t>(a, digit_bits, passes, keys, perm, st)
+                              : sort_in_cluster<int64_t>(a, digit_bits, passes, keys, perm, st);
+    else
+        err = a.id_bits == 32 ? sort_in_tiles<int32_t>(a, digit_bits, passes, base, w, &keys, &perm, st)
+                              : sort_in_tiles<int64_t>(a, digit_bits, passes, base, w, &keys, &perm, st);
     if (err != cudaSuccess) return err;
     return with_type(a.in_type, [&](auto tv) {
         using T = decltype(tv);
@@ -185,11 +653,30 @@ cudaError_t embed_backward(const EmbedArgs& a, const void* gy, int64_t gy_stride
             using O = decltype(ov);
             return with_width<T, O>(a.C, dtable, a.C, gy, gy_stride, [&](auto wv) {
                 constexpr int VE = decltype(wv)::value;
-                const dim3 grid(cdiv(a.V, 8), cdiv(a.C, 32 * VE));
-                embed_bwd_kernel<T, O, VE><<<grid, dim3(32, 8), 0, st>>>(ptr, perm, a.V, a.C,
-                                                                        static_cast<const O*>(gy), gy_stride, a.scale,
-                                                                        static_cast<T*>(dtable));
+                const SumShape s = sum_shape(a.N, a.C, VE);
+                SumParams p{};
+                p.keys = keys;
+                p.perm = perm;
+                p.N = (int)a.N;
+                p.C = a.C;
+                p.R = s.R;
+                p.tiles = s.tiles;
+                p.slabs = s.slabs;
+                p.lx_log2 = s.lx_log2;
+                p.V = a.V;
+                p.ldg = gy_stride;
+                p.scale = a.scale;
+                p.part = reinterpret_cast<float*>(base + w.part);
+                p.sum_blocks = cdiv(((int64_t)s.tiles * s.slabs) << s.lx_log2, 256);
+                const int64_t row = (int64_t)a.C * sizeof(T), zr = 65536 / row;      // 64 KB of rows a block
+                p.zero_rows = (int)(zr < 1 ? 1 : zr > 256 ? 256 : zr);
+                embed_sum_kernel<T, O, VE><<<p.sum_blocks + cdiv(a.V, p.zero_rows), 256, 0, st>>>(
+                    p, static_cast<const O*>(gy), static_cast<T*>(dtable));
                 count_launch();
+                if (s.tiles > 1) {
+                    embed_join_kernel<T, VE><<<dim3(s.tiles - 1, s.slabs), 256, 0, st>>>(p, static_cast<T*>(dtable));
+                    count_launch();
+                }
                 return cudaGetLastError();
             });
         });

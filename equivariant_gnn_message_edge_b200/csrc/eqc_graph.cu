@@ -272,13 +272,6 @@ cudaError_t build_csr(const int* keys, int N, int E, int* ptr, int* perm, char* 
 
 size_t graph_workspace_bytes(int N, int E) { return layout(N, E).total; }
 
-size_t csr_workspace_bytes(int N, int E) { return layout(N, E).total; }
-
-cudaError_t csr_build(const int* keys, int N, int E, int* ptr, int* perm, char* ws, unsigned* status,
-                      cudaStream_t st) {
-    return build_csr(keys, N, E, ptr, perm, ws, status, st);
-}
-
 cudaError_t graph_build(int N, int E, const int* senders, const int* receivers, int* recv_ptr, int* recv_perm,
                         int* send_ptr, int* send_perm, void* ws, unsigned* status, cudaStream_t st) {
     cudaError_t err = build_csr(receivers, N, E, recv_ptr, recv_perm, static_cast<char*>(ws), status, st);

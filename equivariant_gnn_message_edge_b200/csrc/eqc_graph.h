@@ -12,11 +12,6 @@ size_t graph_workspace_bytes(int N, int E);
 cudaError_t graph_build(int N, int E, const int* senders, const int* receivers, int* recv_ptr, int* recv_perm,
                         int* send_ptr, int* send_perm, void* ws, unsigned* status, cudaStream_t st);
 
-// One CSR: ptr[N + 1] and the stable permutation perm[E] of keys[E] in [0, N).
-size_t csr_workspace_bytes(int N, int E);
-cudaError_t csr_build(const int* keys, int N, int E, int* ptr, int* perm, char* ws, unsigned* status,
-                      cudaStream_t st);
-
 // Size of the library's fixed scratch array for graph_build_noalloc.
 constexpr size_t kGraphScratchBytes = size_t(8) << 20;
 
