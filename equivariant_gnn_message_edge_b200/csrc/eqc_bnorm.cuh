@@ -1,0 +1,641 @@
+// Block norm: the root-mean-square norms before and after a layer, fused with
+// the layer's gate, its residual scale and the residual sum.
+//
+// A node's rows of one degree l (2l + 1 rows of C channels, contiguous) are
+// normalised on their own, so the work splits into groups (node, l) that share
+// nothing but the weights w[l, :].  With M = (2l + 1) C, mean over the group:
+//   s_b = rsqrt(mean b^2 + eps)            u = b s_b w_post
+//   y   = x + scale a(gate) u  (= x_out)   s_y = rsqrt(mean y^2 + eps)   h = y s_y w_pre
+// and backward, from g_x and g_h (gradients of x_out and h):
+//   p = g_h w_pre     t = g_x + s_y (p - y s_y^2 mean(p y))      dx = t
+//   q = scale a(gate) t w_post     db = s_b (q - b s_b^2 mean(q b))
+//   dgate[c] = scale a'(gate) sum_m t u
+//   dw_post[l, c] = sum over nodes, m of scale a(gate) t b s_b
+//   dw_pre[l, c]  = sum over nodes, m of g_h y s_y
+// y is made again from x, b and gate, so the backward reads no saved tensor
+// but the two statistics of each group.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "eqc_elem.cuh"
+#include "eqc_layers.h"
+
+namespace eqc {
+
+void count_launch();
+
+namespace bn {
+
+constexpr int kSMs = 148;
+constexpr int kStreamCtas = 4 * kSMs;
+
+struct BnParams {
+    int N, C, L;
+    int first[5];        // CTAs of degree l: [first[l], first[l + 1])
+    int gate_kind;
+    float eps, scale;
+    const void *x, *b, *gate;
+    const float *w_post, *w_pre;
+    void *x_out, *h;
+    float* stats;        // [2][N][L + 1]: s_b, then s_y
+    const void *g_x, *g_h;
+    void *dx, *db, *dgate;
+    float* part;         // [CTAs][2][C]: dw_post, dw_pre
+    int width;           // threads across the channels of a group (a power of two up to 32, or whole warps)
+};
+
+// a(g) and a'(g) of the gate kinds (EQCONV_GATE_*).
+__device__ __forceinline__ void gate_value(int kind, float g, float& a, float& da) {
+    if (kind == 3) {
+        a = tanhf(g);
+        da = 1.f - a * a;
+    } else {
+        const float s = 1.f / (1.f + expf(-g));
+        a = kind == 1 ? s : g * s;
+        da = kind == 1 ? s * (1.f - s) : s * (1.f + g * (1.f - s));
+    }
+}
+
+__device__ __forceinline__ float block_sum(float v, float* red) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.f;
+    for (int w = 0; w < (int)blockDim.x / 32; ++w) v += red[w];
+    return v;
+}
+
+// The degree and the first group of this CTA.
+__device__ __forceinline__ int degree_of(const BnParams& p, int cta) {
+    int l = 0;
+    while (l < p.L && cta >= p.first[l + 1]) ++l;
+    return l;
+}
+
+// Streaming forward: one CTA walks nodes of one degree, three passes over a
+// group's channels (the later ones hit L1 or L2).
+template <class T>
+__global__ void __launch_bounds__(256) bn_fwd_stream(const BnParams p) {
+    __shared__ float red[8];
+    const int l = degree_of(p, blockIdx.x), K = 2 * l + 1, D = (p.L + 1) * (p.L + 1);
+    const int step = p.first[l + 1] - p.first[l];
+    const T* x_ = static_cast<const T*>(p.x);
+    const T* b_ = static_cast<const T*>(p.b);
+    const T* g_ = static_cast<const T*>(p.gate);
+    const float inv_m = 1.f / ((float)K * (float)p.C);
+    for (int n = blockIdx.x - p.first[l]; n < p.N; n += step) {
+        const int64_t at = ((int64_t)n * D + l * l) * p.C, ga = ((int64_t)n * (p.L + 1) + l) * p.C;
+        float sb = 0.f;
+        if (b_) {
+            float s = 0.f;
+            for (int c = threadIdx.x; c < p.C; c += 256)
+                for (int m = 0; m < K; ++m) {
+                    const float v = to_float(b_[at + (int64_t)m * p.C + c]);
+                    s += v * v;
+                }
+            sb = rsqrtf(block_sum(s, red) * inv_m + p.eps);
+        }
+        float s = 0.f;
+        for (int pass = 0; pass < 2; ++pass) {
+            if (pass == 1 && !p.w_pre) break;
+            float sy = 0.f;
+            if (pass == 1) sy = rsqrtf(block_sum(s, red) * inv_m + p.eps);
+            for (int c = threadIdx.x; c < p.C; c += 256) {
+                float a = 1.f, da;
+                if (g_) gate_value(p.gate_kind, to_float(g_[ga + c]), a, da);
+                const float k = b_ ? p.scale * a * sb * p.w_post[l * p.C + c] : 0.f;
+                for (int m = 0; m < K; ++m) {
+                    const int64_t i = at + (int64_t)m * p.C + c;
+                    float y = to_float(x_[i]);
+                    if (b_) y += k * to_float(b_[i]);
+                    if (pass == 0) {
+                        s += y * y;
+                        if (p.x_out) static_cast<T*>(p.x_out)[i] = from_float<T>(y);
+                    } else {
+                        static_cast<T*>(p.h)[i] = from_float<T>(y * sy * p.w_pre[l * p.C + c]);
+                    }
+                }
+            }
+            if (pass == 1 && p.stats && threadIdx.x == 0)
+                p.stats[((int64_t)p.N + n) * (p.L + 1) + l] = sy;
+        }
+        if (p.stats && b_ && threadIdx.x == 0) p.stats[(int64_t)n * (p.L + 1) + l] = sb;
+    }
+}
+
+// Streaming backward: the weight gradients of the CTA's nodes are summed in
+// shared memory, each channel by the thread that owns it.
+template <class T>
+__global__ void __launch_bounds__(256) bn_bwd_stream(const BnParams p) {
+    extern __shared__ float acc[];   // [2][C]
+    __shared__ float red[8];
+    const int l = degree_of(p, blockIdx.x), K = 2 * l + 1, D = (p.L + 1) * (p.L + 1);
+    const int step = p.first[l + 1] - p.first[l];
+    const T* x_ = static_cast<const T*>(p.x);
+    const T* b_ = static_cast<const T*>(p.b);
+    const T* g_ = static_cast<const T*>(p.gate);
+    const T* gx_ = static_cast<const T*>(p.g_x);
+    const T* gh_ = static_cast<const T*>(p.g_h);
+    const float inv_m = 1.f / ((float)K * (float)p.C);
+    for (int c = threadIdx.x; c < 2 * p.C; c += 256) acc[c] = 0.f;
+    __syncthreads();
+    for (int n = blockIdx.x - p.first[l]; n < p.N; n += step) {
+        const int64_t at = ((int64_t)n * D + l * l) * p.C, ga = ((int64_t)n * (p.L + 1) + l) * p.C;
+        const float sb = b_ ? p.stats[(int64_t)n * (p.L + 1) + l] : 0.f;
+        const float sy = gh_ ? p.stats[((int64_t)p.N + n) * (p.L + 1) + l] : 0.f;
+        float mean_py = 0.f, mean_qb = 0.f;
+        for (int pass = gh_ ? 0 : 1; pass < 3; ++pass) {
+            if (pass == 2 && !b_) break;
+            float s = 0.f;
+            for (int c = threadIdx.x; c < p.C; c += 256) {
+                float a = 1.f, da = 0.f;
+                if (g_) gate_value(p.gate_kind, to_float(g_[ga + c]), a, da);
+                const float wo = b_ ? p.w_post[l * p.C + c] : 0.f;
+                const float wi = gh_ ? p.w_pre[l * p.C + c] : 0.f;
+                const float k = p.scale * a * sb * wo;
+                float tb = 0.f, gy = 0.f;
+                for (int m = 0; m < K; ++m) {
+                    const int64_t i = at + (int64_t)m * p.C + c;
+                    const float b = b_ ? to_float(b_[i]) : 0.f;
+                    float t = gx_ ? to_float(gx_[i]) : 0.f;
+                    if (gh_) {
+                        float y = to_float(x_[i]);
+                        if (b_) y += k * b;
+                        const float gh = to_float(gh_[i]), pp = gh * wi;
+                        if (pass == 0) s += pp * y;
+                        gy += gh * y;
+                        t += sy * (pp - y * (sy * sy) * mean_py);
+                    }
+                    if (pass == 1) {
+                        static_cast<T*>(p.dx)[i] = from_float<T>(t);
+                        tb += t * b;
+                        s += p.scale * a * t * wo * b;
+                    } else if (pass == 2) {
+                        const float q = p.scale * a * t * wo;
+                        static_cast<T*>(p.db)[i] = from_float<T>(sb * (q - b * (sb * sb) * mean_qb));
+                    }
+                }
+                if (pass == 1) {
+                    if (g_) static_cast<T*>(p.dgate)[ga + c] = from_float<T>(p.scale * da * tb * sb * wo);
+                    acc[c] += p.scale * a * tb * sb;
+                    acc[p.C + c] += gy * sy;
+                }
+            }
+            if (pass == 0) mean_py = block_sum(s, red) * inv_m;
+            if (pass == 1 && b_) mean_qb = block_sum(s, red) * inv_m;
+        }
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * p.C; c += 256) p.part[(int64_t)blockIdx.x * 2 * p.C + c] = acc[c];
+}
+
+
+// ---------------------------------------------------------------------------
+// Resident kernels: a group's elements stay in registers between the sums.
+// A worker (p.width threads: part of a warp, a warp, or a whole CTA of warps)
+// owns a group; a thread owns V neighbouring channels (16 bytes where the rows
+// allow it), J times p.width V channels apart, in all K = 2l + 1 rows, of NB
+// nodes at a time.  Bound by memory: every tensor is moved once, and a worker
+// has all loads of its NB groups in flight together.  The weights and the sums
+// of their gradients stay in the thread that owns the channel for the whole
+// persistent loop over nodes.
+
+// Sums of NB values over the worker's threads; every thread gets them.
+template <int NB>
+struct WorkerSum {
+    float* red;          // [2][NB][16], only for workers of several warps
+    int width, flip;
+    __device__ __forceinline__ void operator()(float (&v)[NB]) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+            if (o < width)
+#pragma unroll
+                for (int i = 0; i < NB; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        if (width <= 32) return;
+        const int warps = width >> 5;
+        float* r = red + flip * NB * 16;
+        flip ^= 1;       // the next sum's buffer: one barrier a sum is enough
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int i = 0; i < NB; ++i) r[i * 16 + (threadIdx.x >> 5)] = v[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            float s = 0.f;
+            for (int w = 0; w < warps; ++w) s += r[i * 16 + w];
+            v[i] = s;
+        }
+    }
+};
+
+// Nodes at a time: more where a group is small, within the registers.
+template <int V, int K, int J, bool BWD>
+constexpr int batch_of() {
+    return BWD ? (K * J == 1 && V < 8 ? 2 : 1) : K * J >= 4 ? 1 : (K * J >= 2 || V == 8) ? 2 : 4;
+}
+
+template <class T, int V, int K, int J>
+__device__ __forceinline__ void fwd_groups(const BnParams& p, int l, float* red) {
+    constexpr int NB = batch_of<V, K, J, false>();
+    const int D = (p.L + 1) * (p.L + 1);
+    const int workers = p.width <= 32 ? (int)blockDim.x / p.width : 1;
+    const int worker = p.width <= 32 ? threadIdx.x / p.width : 0;
+    const int x0 = threadIdx.x - worker * p.width;
+    const bool post = p.b != nullptr, pre = p.w_pre != nullptr, gated = p.gate != nullptr;
+    const float inv_m = 1.f / ((float)K * (float)p.C);
+    const int64_t step = (int64_t)(p.first[l + 1] - p.first[l]) * workers * NB;
+    WorkerSum<NB> sum{red, p.width, 0};
+    Pack<float, V> wo[J], wi[J];
+    bool own[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const int c = (x0 + j * p.width) * V;
+        own[j] = c < p.C;
+        if (own[j] && post)
+#pragma unroll
+            for (int e = 0; e < V; ++e) wo[j].e[e] = __ldg(p.w_post + l * p.C + c + e);
+        if (own[j] && pre)
+#pragma unroll
+            for (int e = 0; e < V; ++e) wi[j].e[e] = __ldg(p.w_pre + l * p.C + c + e);
+    }
+    for (int64_t n0 = (int64_t)(blockIdx.x - p.first[l]) * workers * NB; n0 < p.N; n0 += step) {
+        Pack<T, V> x[NB][K][J], b[NB][K][J], g[NB][J];
+        const int64_t nw = n0 + worker * NB;
+        const auto at = [&](int i, int m, int j) {
+            return ((nw + i) * D + l * l + m) * p.C + (x0 + j * p.width) * V;
+        };
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if (!own[j] || nw + i >= p.N) continue;
+#pragma unroll
+                for (int m = 0; m < K; ++m) {
+                    x[i][m][j].load(static_cast<const T*>(p.x) + at(i, m, j));
+                    if (post) b[i][m][j].load(static_cast<const T*>(p.b) + at(i, m, j));
+                }
+                if (gated)
+                    g[i][j].load(static_cast<const T*>(p.gate) + ((nw + i) * (p.L + 1) + l) * p.C + (x0 + j * p.width) * V);
+            }
+        float sb[NB], sy[NB];
+#pragma unroll
+        for (int i = 0; i < NB; ++i) sb[i] = sy[i] = 0.f;
+        if (post) {
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+                    if (own[j] && nw + i < p.N)
+#pragma unroll
+                        for (int m = 0; m < K; ++m)
+#pragma unroll
+                            for (int e = 0; e < V; ++e) sb[i] += b[i][m][j].get(e) * b[i][m][j].get(e);
+            sum(sb);
+#pragma unroll
+            for (int i = 0; i < NB; ++i) sb[i] = rsqrtf(sb[i] * inv_m + p.eps);
+        }
+        float k[NB][J][V];        // y = x + k b
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if (!own[j] || nw + i >= p.N) continue;
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    float a = 1.f, da;
+                    if (gated) gate_value(p.gate_kind, g[i][j].get(e), a, da);
+                    k[i][j][e] = post ? p.scale * a * sb[i] * wo[j].e[e] : 0.f;
+                }
+#pragma unroll
+                for (int m = 0; m < K; ++m) {
+                    Pack<T, V> o;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        float y = x[i][m][j].get(e);
+                        if (post) y += k[i][j][e] * b[i][m][j].get(e);
+                        sy[i] += y * y;
+                        o.set(e, y);
+                    }
+                    if (post) o.store(static_cast<T*>(p.x_out) + at(i, m, j));
+                }
+            }
+        if (pre) {
+            sum(sy);
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                sy[i] = rsqrtf(sy[i] * inv_m + p.eps);
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    if (!own[j] || nw + i >= p.N) continue;
+#pragma unroll
+                    for (int m = 0; m < K; ++m) {
+                        Pack<T, V> o;
+#pragma unroll
+                        for (int e = 0; e < V; ++e) {
+                            float y = x[i][m][j].get(e);
+                            if (post) y += k[i][j][e] * b[i][m][j].get(e);
+                            o.set(e, y * sy[i] * wi[j].e[e]);
+                        }
+                        o.store(static_cast<T*>(p.h) + at(i, m, j));
+                    }
+                }
+            }
+        }
+        if (p.stats && x0 == 0)
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+                if (nw + i < p.N) {
+                    if (post) p.stats[(nw + i) * (p.L + 1) + l] = sb[i];
+                    if (pre) p.stats[((int64_t)p.N + nw + i) * (p.L + 1) + l] = sy[i];
+                }
+    }
+}
+
+template <class T, int V, int K, int J>
+__device__ __forceinline__ void bwd_groups(const BnParams& p, int l, float* red, float* dw) {
+    constexpr int NB = batch_of<V, K, J, true>();
+    const int D = (p.L + 1) * (p.L + 1);
+    const int workers = p.width <= 32 ? (int)blockDim.x / p.width : 1;
+    const int worker = p.width <= 32 ? threadIdx.x / p.width : 0;
+    const int x0 = threadIdx.x - worker * p.width;
+    const bool post = p.b != nullptr, pre = p.g_h != nullptr, gated = p.gate != nullptr, more = p.g_x != nullptr;
+    const float inv_m = 1.f / ((float)K * (float)p.C);
+    const int64_t step = (int64_t)(p.first[l + 1] - p.first[l]) * workers * NB;
+    WorkerSum<NB> sum{red, p.width, 0};
+    Pack<float, V> wo[J], wi[J];
+    float dwo[J][V], dwi[J][V];
+    bool own[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const int c = (x0 + j * p.width) * V;
+        own[j] = c < p.C;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            dwo[j][e] = dwi[j][e] = 0.f;
+            wo[j].e[e] = own[j] && post ? __ldg(p.w_post + l * p.C + c + e) : 0.f;
+            wi[j].e[e] = own[j] && pre ? __ldg(p.w_pre + l * p.C + c + e) : 0.f;
+        }
+    }
+    for (int64_t n0 = (int64_t)(blockIdx.x - p.first[l]) * workers * NB; n0 < p.N; n0 += step) {
+        Pack<T, V> x[NB][K][J], b[NB][K][J], gx[NB][K][J], gh[NB][K][J], g[NB][J];
+        float sb[NB], sy[NB];
+        const int64_t nw = n0 + worker * NB;
+        const auto at = [&](int i, int m, int j) {
+            return ((nw + i) * D + l * l + m) * p.C + (x0 + j * p.width) * V;
+        };
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            sb[i] = post && nw + i < p.N ? __ldg(p.stats + (nw + i) * (p.L + 1) + l) : 0.f;
+            sy[i] = pre && nw + i < p.N ? __ldg(p.stats + ((int64_t)p.N + nw + i) * (p.L + 1) + l) : 0.f;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if (!own[j] || nw + i >= p.N) continue;
+#pragma unroll
+                for (int m = 0; m < K; ++m) {
+                    if (pre) x[i][m][j].load(static_cast<const T*>(p.x) + at(i, m, j));
+                    if (post) b[i][m][j].load(static_cast<const T*>(p.b) + at(i, m, j));
+                    if (more) gx[i][m][j].load(static_cast<const T*>(p.g_x) + at(i, m, j));
+                    if (pre) gh[i][m][j].load(static_cast<const T*>(p.g_h) + at(i, m, j));
+                }
+                if (gated)
+                    g[i][j].load(static_cast<const T*>(p.gate) + ((nw + i) * (p.L + 1) + l) * p.C + (x0 + j * p.width) * V);
+            }
+        }
+        float sa[NB][J][V], da[NB][J][V];      // scale a(gate), scale a'(gate)
+        float mpy[NB], mqb[NB];
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            mpy[i] = mqb[i] = 0.f;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if (!own[j] || nw + i >= p.N) continue;
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    float a = 1.f, d = 0.f;
+                    if (gated) gate_value(p.gate_kind, g[i][j].get(e), a, d);
+                    sa[i][j][e] = p.scale * a;
+                    da[i][j][e] = p.scale * d;
+                }
+                if (pre)
+#pragma unroll
+                    for (int m = 0; m < K; ++m)
+#pragma unroll
+                        for (int e = 0; e < V; ++e) {
+                            float y = x[i][m][j].get(e);
+                            if (post) y += sa[i][j][e] * sb[i] * wo[j].e[e] * b[i][m][j].get(e);
+                            mpy[i] += gh[i][m][j].get(e) * wi[j].e[e] * y;
+                        }
+            }
+        }
+        if (pre) {
+            sum(mpy);
+#pragma unroll
+            for (int i = 0; i < NB; ++i) mpy[i] *= inv_m * sy[i] * sy[i];
+        }
+        // t, the gradient of x_out in all
+        const auto grad = [&](int i, int m, int j, int e) {
+            float t = more ? gx[i][m][j].get(e) : 0.f;
+            if (pre) {
+                float y = x[i][m][j].get(e);
+                if (post) y += sa[i][j][e] * sb[i] * wo[j].e[e] * b[i][m][j].get(e);
+                t += sy[i] * (gh[i][m][j].get(e) * wi[j].e[e] - y * mpy[i]);
+            }
+            return t;
+        };
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if (!own[j] || nw + i >= p.N) continue;
+                float tb[V], gy[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e) tb[e] = gy[e] = 0.f;
+#pragma unroll
+                for (int m = 0; m < K; ++m) {
+                    Pack<T, V> o;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        const float t = grad(i, m, j, e);
+                        o.set(e, t);
+                        if (post) tb[e] += t * b[i][m][j].get(e);
+                        if (pre) {
+                            float y = x[i][m][j].get(e);
+                            if (post) y += sa[i][j][e] * sb[i] * wo[j].e[e] * b[i][m][j].get(e);
+                            gy[e] += gh[i][m][j].get(e) * y;
+                        }
+                    }
+                    o.store(static_cast<T*>(p.dx) + at(i, m, j));
+                }
+                Pack<T, V> o;
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    mqb[i] += sa[i][j][e] * wo[j].e[e] * tb[e];
+                    dwo[j][e] += sa[i][j][e] * sb[i] * tb[e];
+                    dwi[j][e] += sy[i] * gy[e];
+                    o.set(e, da[i][j][e] * sb[i] * wo[j].e[e] * tb[e]);
+                }
+                if (gated)
+                    o.store(static_cast<T*>(p.dgate) + ((nw + i) * (p.L + 1) + l) * p.C + (x0 + j * p.width) * V);
+            }
+        if (!post) continue;
+        sum(mqb);
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            mqb[i] *= inv_m * sb[i] * sb[i];
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if (!own[j] || nw + i >= p.N) continue;
+#pragma unroll
+                for (int m = 0; m < K; ++m) {
+                    Pack<T, V> o;
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        o.set(e, sb[i] * (sa[i][j][e] * wo[j].e[e] * grad(i, m, j, e) - b[i][m][j].get(e) * mqb[i]));
+                    o.store(static_cast<T*>(p.db) + at(i, m, j));
+                }
+            }
+        }
+    }
+    // the CTA's sums: its workers' in order
+    float* part = p.part + (int64_t)blockIdx.x * 2 * p.C;
+    if (workers == 1) {
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            if (own[j])
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    part[(x0 + j * p.width) * V + e] = dwo[j][e];
+                    part[p.C + (x0 + j * p.width) * V + e] = dwi[j][e];
+                }
+        return;
+    }
+    // several workers: width <= 32 and J = 1, at most 128 x V x 2 values
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        dw[(threadIdx.x * 2) * V + e] = dwo[0][e];
+        dw[(threadIdx.x * 2 + 1) * V + e] = dwi[0][e];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * p.width * V; i += blockDim.x) {
+        const int which = i / (p.width * V), c = i - which * p.width * V;
+        if (c >= p.C) continue;
+        float s = 0.f;
+        for (int w = 0; w < workers; ++w) s += dw[((w * p.width + c / V) * 2 + which) * V + c % V];
+        part[which * p.C + c] = s;
+    }
+}
+
+// LMAX: the plan's L; J > 1 only for L = 0.  One CTA works on one degree.
+template <class T, int V, int LMAX, int J>
+__global__ void __launch_bounds__(LMAX == 0 ? 512 : 256) bn_fwd_kernel(const BnParams p) {
+    __shared__ float red[2 * 4 * 16];
+    const int l = degree_of(p, blockIdx.x);
+    if (l == 0) return fwd_groups<T, V, 1, J>(p, 0, red);
+    if constexpr (LMAX >= 1)
+        if (l == 1) return fwd_groups<T, V, 3, 1>(p, 1, red);
+    if constexpr (LMAX >= 2)
+        if (l == 2) return fwd_groups<T, V, 5, 1>(p, 2, red);
+    if constexpr (LMAX >= 3) return fwd_groups<T, V, 7, 1>(p, 3, red);
+}
+
+template <class T, int V, int LMAX, int J>
+__global__ void __launch_bounds__(LMAX == 0 ? 512 : 256) bn_bwd_kernel(const BnParams p) {
+    __shared__ float red[2 * 4 * 16];
+    __shared__ float dw[128 * 2 * V];
+    const int l = degree_of(p, blockIdx.x);
+    if (l == 0) return bwd_groups<T, V, 1, J>(p, 0, red, dw);
+    if constexpr (LMAX >= 1)
+        if (l == 1) return bwd_groups<T, V, 3, 1>(p, 1, red, dw);
+    if constexpr (LMAX >= 2)
+        if (l == 2) return bwd_groups<T, V, 5, 1>(p, 2, red, dw);
+    if constexpr (LMAX >= 3) return bwd_groups<T, V, 7, 1>(p, 3, red, dw);
+}
+
+// How a launch is cut: V channels a thread (0: the streaming kernels), J
+// times, `width` threads a group, `threads` a CTA.
+struct Shape {
+    int V, J, width, threads;
+};
+
+// The widest vector that divides C and every pointer allows, then the fewest
+// channels a thread that fit: up to 512 threads x 4 vectors for L = 0, and
+// 256 threads x 1 for L > 0, whose groups hold up to 7 rows in registers.
+inline Shape shape_of(int L, int C, int V) {
+    Shape s{V, 1, 0, 0};
+    const int vecs = C / V, most = L == 0 ? 512 : 256;
+    while (s.J < (L == 0 ? 4 : 1) && (vecs + s.J - 1) / s.J > most) s.J *= 2;
+    const int across = (vecs + s.J - 1) / s.J;
+    if (across > most) return Shape{0, 0, 0, 0};
+    if (across > 32) {
+        s.width = s.threads = (across + 31) / 32 * 32;
+    } else {
+        s.width = 1;
+        while (s.width < across) s.width *= 2;
+        s.threads = 128;
+    }
+    return s;
+}
+
+// CTAs in proportion to what the degrees move, at least one each and no more
+// than there are batches of nodes.
+inline void split_ctas(BnParams& p, int most, int nodes_per_cta) {
+    const int D = (p.L + 1) * (p.L + 1);
+    const int64_t batches = ((int64_t)p.N + nodes_per_cta - 1) / nodes_per_cta;
+    p.first[0] = 0;
+    for (int l = 0; l <= p.L; ++l) {
+        int64_t k = (int64_t)most * (2 * l + 1) / D;
+        if (k > batches) k = batches;
+        if (k < 1) k = 1;
+        p.first[l + 1] = p.first[l] + (int)k;
+    }
+}
+
+// Most CTAs an SM runs of a launch; partial sums are sized by it.
+inline int cta_cap(const Shape& s) {
+    if (!s.V) return kStreamCtas / kSMs;
+    const int k = 1024 / s.threads;
+    return k < 1 ? 1 : k > 8 ? 8 : k;
+}
+
+template <class T, int V, int LMAX, int J, bool BWD>
+cudaError_t launch(BnParams& p, const Shape& s, cudaStream_t st) {
+    void (*kernel)(BnParams) = nullptr;
+    if constexpr (BWD) kernel = bn_bwd_kernel<T, V, LMAX, J>;
+    else kernel = bn_fwd_kernel<T, V, LMAX, J>;
+    static int regs = 0;                     // of this kernel, asked for once
+    if (!regs) {
+        cudaFuncAttributes a;
+        const cudaError_t e = cudaFuncGetAttributes(&a, kernel);
+        if (e != cudaSuccess) return e;
+        regs = a.numRegs;
+    }
+    int resident = 65536 / (((regs + 7) / 8 * 8) * s.threads);
+    resident = resident < 1 ? 1 : resident;
+    const int cap = cta_cap(s);
+    p.width = s.width;
+    split_ctas(p, kSMs * (resident < cap ? resident : cap), s.width <= 32 ? s.threads / s.width : 1);
+    kernel<<<p.first[p.L + 1], s.threads, 0, st>>>(p);
+    count_launch();
+    return cudaGetLastError();
+}
+
+template <class T, int V, bool BWD>
+cudaError_t launch_for(BnParams& p, const Shape& s, cudaStream_t st) {
+    if (p.L == 0) {
+        if (s.J == 1) return launch<T, V, 0, 1, BWD>(p, s, st);
+        if (s.J == 2) return launch<T, V, 0, 2, BWD>(p, s, st);
+        return launch<T, V, 0, 4, BWD>(p, s, st);
+    }
+    if (p.L == 1) return launch<T, V, 1, 1, BWD>(p, s, st);
+    if (p.L == 2) return launch<T, V, 2, 1, BWD>(p, s, st);
+    return launch<T, V, 3, 1, BWD>(p, s, st);
+}
+
+}  // namespace bn
+}  // namespace eqc

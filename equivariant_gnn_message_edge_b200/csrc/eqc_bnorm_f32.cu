@@ -1,0 +1,3 @@
+#define EQC_BN_TYPE float
+#define EQC_BN_NAME run_f32
+#include "eqc_bnorm_inst.cuh"

@@ -1,0 +1,31 @@
+// Instances of the block norm for one element type: EQC_BN_TYPE, EQC_BN_NAME.
+// p.first receives the CTAs of each degree.
+#include "eqc_bnorm.cuh"
+
+namespace eqc {
+namespace bn {
+
+cudaError_t EQC_BN_NAME(BnParams& p, const Shape& s, bool bwd, cudaStream_t st) {
+    using T = EQC_BN_TYPE;
+    constexpr int kWide = 16 / sizeof(T);
+    if (s.V == kWide) return bwd ? launch_for<T, kWide, true>(p, s, st) : launch_for<T, kWide, false>(p, s, st);
+    if (s.V == 2) return bwd ? launch_for<T, 2, true>(p, s, st) : launch_for<T, 2, false>(p, s, st);
+    if (s.V == 1) return bwd ? launch_for<T, 1, true>(p, s, st) : launch_for<T, 1, false>(p, s, st);
+    split_ctas(p, kStreamCtas, 1);
+    if (bwd) {
+        const int smem = 2 * p.C * (int)sizeof(float);
+        if (smem > 40 * 1024) {
+            const cudaError_t e =
+                cudaFuncSetAttribute(bn_bwd_stream<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return e;
+        }
+        bn_bwd_stream<T><<<p.first[p.L + 1], 256, smem, st>>>(p);
+    } else {
+        bn_fwd_stream<T><<<p.first[p.L + 1], 256, 0, st>>>(p);
+    }
+    count_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace bn
+}  // namespace eqc
