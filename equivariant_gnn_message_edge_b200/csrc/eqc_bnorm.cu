@@ -1,6 +1,6 @@
 // Host side of the block norm: the shape of a launch, and the weight gradients'
 // last sum (kernels in eqc_bnorm.cuh, instances in eqc_bnorm_<type>.cu).
-#include "eqc_bnorm.cuh"
+#include "eqc_bnorm_staged.cuh"
 
 namespace eqc {
 namespace bn {
@@ -8,22 +8,28 @@ namespace bn {
 cudaError_t run_f32(BnParams& p, const Shape& s, bool bwd, cudaStream_t st);
 cudaError_t run_bf16(BnParams& p, const Shape& s, bool bwd, cudaStream_t st);
 cudaError_t run_f16(BnParams& p, const Shape& s, bool bwd, cudaStream_t st);
+cudaError_t staged_f32(const StagedParams& s, const Staged& h, int grid, bool bwd, cudaStream_t st);
+cudaError_t staged_bf16(const StagedParams& s, const Staged& h, int grid, bool bwd, cudaStream_t st);
+cudaError_t staged_f16(const StagedParams& s, const Staged& h, int grid, bool bwd, cudaStream_t st);
 
 namespace {
 
 // dw[l, c]: the CTAs' partial rows in CTA order, 8 equal runs of them by the
-// block's 8 warps and the warps' sums in order.
-__global__ void __launch_bounds__(256) bn_dw_reduce(const BnParams p, float* dw_post, float* dw_pre) {
+// block's 8 warps and the warps' sums in order.  rows: degrees a CTA has sums
+// of (L + 1, or 1 where CTAs first[l] .. first[l + 1] work on degree l).
+__global__ void __launch_bounds__(256) bn_dw_reduce(const BnParams p, int rows, float* dw_post, float* dw_pre) {
     __shared__ float s[8][32];
     const int x = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + x, l = blockIdx.y;
     float* dw = blockIdx.z ? dw_pre : dw_post;
     if (!dw) return;
-    const int share = (p.first[l + 1] - p.first[l] + 7) / 8;
-    const int t0 = p.first[l] + w * share, t1 = t0 + share < p.first[l + 1] ? t0 + share : p.first[l + 1];
+    const int from = rows == 1 ? p.first[l] : 0, to = rows == 1 ? p.first[l + 1] : p.first[p.L + 1];
+    const int share = (to - from + 7) / 8;
+    const int t0 = from + w * share, t1 = t0 + share < to ? t0 + share : to;
     float v = 0.f;
     if (c < p.C)
 #pragma unroll 8
-        for (int t = t0; t < t1; ++t) v += p.part[((int64_t)t * 2 + blockIdx.z) * p.C + c];
+        for (int t = t0; t < t1; ++t)
+            v += p.part[(((int64_t)t * 2 + blockIdx.z) * rows + (rows == 1 ? 0 : l)) * p.C + c];
     s[w][x] = v;
     __syncthreads();
     if (w != 0 || c >= p.C) return;
@@ -69,8 +75,56 @@ Shape shape_for(const BlockNormArgs& a) {
     return Shape{0, 0, 0, 0};
 }
 
-cudaError_t run(BnParams& p, const BlockNormArgs& a, bool bwd, cudaStream_t st) {
+// The staged launch of these arguments (slots 0: none).
+Staged staged_for_args(const BlockNormArgs& a, bool bwd) {
+    uintptr_t all = 0;
+    for (const void* q : {a.x, a.b, a.gate, (const void*)a.x_out, (const void*)a.h, a.g_x, a.g_h,
+                          (const void*)a.dx, (const void*)a.db, (const void*)a.dgate})
+        all |= reinterpret_cast<uintptr_t>(q);
+    if (all % 16 != 0) return Staged{};
+    const int tensors = bwd ? 2 * (a.g_h != nullptr) + (a.b != nullptr) + (a.g_x != nullptr) : 1 + (a.b != nullptr);
+    return tensors ? staged_shape(a.L, a.C, type_bytes(a.type), tensors, a.gate != nullptr) : Staged{};
+}
+
+// rows: of the partial sums a CTA leaves (see bn_dw_reduce).
+cudaError_t run(BnParams& p, const BlockNormArgs& a, bool bwd, cudaStream_t st, int* rows) {
+    const Staged h = staged_for_args(a, bwd);
+    if (h.slots) {
+        StagedParams s{};
+        const int es = type_bytes(a.type);
+        p.width = h.width;
+        s.slots = h.slots;
+        s.nodes = h.nodes;
+        s.total = ((int64_t)a.N + h.nodes - 1) / h.nodes;
+        s.node_bytes = (a.L + 1) * (a.L + 1) * a.C * es;
+        s.gate_bytes = a.gate ? (a.L + 1) * a.C * es : 0;
+        int o = 0;
+        const auto place = [&](bool there) {
+            const int at = o;
+            if (there) o += s.node_bytes * h.nodes;
+            return at;
+        };
+        s.o_x = place(!bwd || a.g_h);
+        s.o_b = place(a.b);
+        s.o_gx = place(bwd && a.g_x);
+        s.o_gh = place(bwd && a.g_h);
+        s.o_g = o;
+        s.slot_bytes = o + s.gate_bytes * h.nodes;
+        s.per_node = s.slot_bytes / h.nodes;
+        s.status = a.status;
+        const int64_t most = (int64_t)kSMs * h.ctas;
+        const int grid = (int)(s.total < most ? s.total : most);
+        p.first[p.L + 1] = grid;
+        s.p = p;
+        *rows = a.L + 1;
+        switch (a.type) {
+            case EQCONV_F32: return staged_f32(s, h, grid, bwd, st);
+            case EQCONV_BF16: return staged_bf16(s, h, grid, bwd, st);
+            default: return staged_f16(s, h, grid, bwd, st);
+        }
+    }
     const Shape s = shape_for(a);
+    *rows = 1;
     switch (a.type) {
         case EQCONV_F32: return run_f32(p, s, bwd, st);
         case EQCONV_BF16: return run_bf16(p, s, bwd, st);
@@ -84,7 +138,8 @@ cudaError_t run(BnParams& p, const BlockNormArgs& a, bool bwd, cudaStream_t st) 
 cudaError_t block_norm_forward(const BlockNormArgs& a, cudaStream_t st) {
     if (a.N == 0) return cudaSuccess;
     bn::BnParams p = bn::params_of(a);
-    return bn::run(p, a, false, st);
+    int rows = 0;
+    return bn::run(p, a, false, st, &rows);
 }
 
 size_t block_norm_workspace(int L, int C, int N) {
@@ -97,7 +152,11 @@ size_t block_norm_workspace(int L, int C, int N) {
     }
     int64_t ctas = (int64_t)bn::kSMs * most;
     if (ctas > (int64_t)N * (L + 1)) ctas = (int64_t)N * (L + 1);
-    return (size_t)(ctas + L + 1) * 2 * C * sizeof(float);
+    // or two CTAs an SM with the sums of all degrees
+    int64_t staged = 2 * (int64_t)bn::kSMs;
+    if (staged > N) staged = N;
+    const int64_t r = ctas + L + 1 > staged * (L + 1) ? ctas + L + 1 : staged * (L + 1);
+    return (size_t)r * 2 * C * sizeof(float);
 }
 
 cudaError_t block_norm_backward(const BlockNormArgs& a, cudaStream_t st) {
@@ -109,8 +168,9 @@ cudaError_t block_norm_backward(const BlockNormArgs& a, cudaStream_t st) {
         return cudaSuccess;
     }
     bn::BnParams p = bn::params_of(a);
-    if ((err = bn::run(p, a, true, st)) != cudaSuccess || (!a.dw_post && !a.dw_pre)) return err;
-    bn::bn_dw_reduce<<<dim3((a.C + 31) / 32, a.L + 1, 2), 256, 0, st>>>(p, a.dw_post, a.dw_pre);
+    int rows = 0;
+    if ((err = bn::run(p, a, true, st, &rows)) != cudaSuccess || (!a.dw_post && !a.dw_pre)) return err;
+    bn::bn_dw_reduce<<<dim3((a.C + 31) / 32, a.L + 1, 2), 256, 0, st>>>(p, rows, a.dw_post, a.dw_pre);
     count_launch();
     return cudaGetLastError();
 }

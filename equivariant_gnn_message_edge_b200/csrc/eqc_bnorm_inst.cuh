@@ -1,6 +1,6 @@
 // Instances of the block norm for one element type: EQC_BN_TYPE, EQC_BN_NAME.
 // p.first receives the CTAs of each degree.
-#include "eqc_bnorm.cuh"
+#include "eqc_bnorm_staged.cuh"
 
 namespace eqc {
 namespace bn {
@@ -25,6 +25,10 @@ cudaError_t EQC_BN_NAME(BnParams& p, const Shape& s, bool bwd, cudaStream_t st) 
     }
     count_launch();
     return cudaGetLastError();
+}
+
+cudaError_t EQC_BN_STAGED(const StagedParams& s, const Staged& h, int grid, bool bwd, cudaStream_t st) {
+    return bwd ? staged_for<EQC_BN_TYPE, true>(s, h, grid, st) : staged_for<EQC_BN_TYPE, false>(s, h, grid, st);
 }
 
 }  // namespace bn

@@ -1,0 +1,528 @@
+// Block norm, staged: whole nodes come to shared memory by bulk copies, a ring
+// of slots ahead of the threads that work on them.  A node's rows of all
+// degrees are contiguous in every tensor, so a slot is one copy per tensor; the
+// copies of the next slots run while the current ones are summed and written,
+// which is what the register-resident kernels of eqc_bnorm.cuh lack (their
+// loads, sums and stores follow one another in each warp).  Used where the
+// tensors are 16-byte aligned, C is whole 16-byte vectors and two slots fit.
+//
+// A worker is a warp (32 / width nodes a slot, several workers share the ring)
+// or, for wide nodes, the whole CTA (one node a slot).  Its threads own V
+// neighbouring channels, J times, of every row of the node.
+#pragma once
+
+#include "eqc_bnorm.cuh"
+#include "eqc_bulk.cuh"
+
+namespace eqc {
+namespace bn {
+
+constexpr int kMaxSlots = 16;
+
+struct StagedParams {
+    BnParams p;
+    int slots, nodes;          // slots of the ring, nodes a slot
+    int64_t total;             // slots' worth of nodes in all
+    // byte offsets of the tensors in a slot, and their bytes a node
+    int o_x, o_b, o_gx, o_gh, o_g, slot_bytes, node_bytes, gate_bytes, per_node;
+    unsigned* status;
+};
+
+struct Ring {
+    unsigned char* base;
+    uint64_t* full;
+};
+
+// Copies of sequence number k of this CTA into its slot, by one thread.
+template <bool BWD>
+__device__ __forceinline__ void fill(const StagedParams& s, const Ring& r, int k) {
+    const int64_t g = blockIdx.x + (int64_t)k * gridDim.x;
+    if (g >= s.total) return;
+    const int64_t n0 = g * s.nodes;
+    const uint32_t nodes = (uint32_t)(s.p.N - n0 < s.nodes ? s.p.N - n0 : s.nodes);
+    const int slot = k % s.slots;
+    unsigned char* d = r.base + (int64_t)slot * s.slot_bytes;
+    uint64_t* bar = r.full + slot;
+    bulk::expect(bar, nodes * (uint32_t)s.per_node);
+    const uint32_t nb = nodes * s.node_bytes;
+    const auto from = [&](const void* p, int64_t bytes) { return static_cast<const unsigned char*>(p) + n0 * bytes; };
+    if (!BWD || s.p.g_h) bulk::copy(d + s.o_x, from(s.p.x, s.node_bytes), nb, bar);
+    if (s.p.b) bulk::copy(d + s.o_b, from(s.p.b, s.node_bytes), nb, bar);
+    if (BWD && s.p.g_x) bulk::copy(d + s.o_gx, from(s.p.g_x, s.node_bytes), nb, bar);
+    if (BWD && s.p.g_h) bulk::copy(d + s.o_gh, from(s.p.g_h, s.node_bytes), nb, bar);
+    if (s.p.gate) bulk::copy(d + s.o_g, from(s.p.gate, s.gate_bytes), nodes * s.gate_bytes, bar);
+}
+
+// What one thread sees of its node: the tensors' slot parts at its channels.
+template <class T>
+struct View {
+    const T *x, *b, *gx, *gh, *g;
+};
+
+template <class T, int V>
+__device__ __forceinline__ void lds(float (&v)[V], const T* p) {
+    Pack<T, V> k;
+    if constexpr (Pack<T, V>::kPiece == 16) {
+#pragma unroll
+        for (int i = 0; i < Pack<T, V>::kBytes / 16; ++i) k.q[i] = reinterpret_cast<const uint4*>(p)[i];
+    } else {
+        static_assert(Pack<T, V>::kPiece == 8, "four 16-bit channels");
+        k.d = *reinterpret_cast<const uint2*>(p);
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = k.get(e);
+}
+
+template <class T, int V>
+__device__ __forceinline__ void put(T* p, const float (&v)[V]) {
+    Pack<T, V> o;
+#pragma unroll
+    for (int e = 0; e < V; ++e) o.set(e, v[e]);
+    o.store(p);
+}
+
+template <class T, int V, int L, int J>
+__device__ __forceinline__ void fwd_node(const BnParams& p, const View<T>& s, const float* w, const bool (&own)[J],
+                                         int cstep, bool live, int64_t row, int64_t grow, int64_t srow, int c0,
+                                         bool lead, WorkerSum<L + 1>& sum) {
+    const bool post = p.b != nullptr, pre = p.w_pre != nullptr, gated = p.gate != nullptr;
+    float sb[L + 1], sy[L + 1];
+#pragma unroll
+    for (int l = 0; l <= L; ++l) sb[l] = sy[l] = 0.f;
+    if (post) {
+#pragma unroll
+        for (int l = 0; l <= L; ++l)
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                if (own[j])
+#pragma unroll
+                    for (int m = 0; m < 2 * l + 1; ++m) {
+                        float b[V];
+                        lds(b, s.b + (l * l + m) * p.C + j * cstep);
+#pragma unroll
+                        for (int e = 0; e < V; ++e) sb[l] += b[e] * b[e];
+                    }
+        sum(sb);
+    }
+    float k[L + 1][J][V];
+#pragma unroll
+    for (int l = 0; l <= L; ++l) {
+        if (post) sb[l] = rsqrtf(sb[l] * (1.f / ((2 * l + 1) * (float)p.C)) + p.eps);
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            if (!own[j]) continue;
+            if (post) {
+                float wo[V];
+                lds(wo, w + l * p.C + c0 + j * cstep);
+#pragma unroll
+                for (int e = 0; e < V; ++e) k[l][j][e] = p.scale * sb[l] * wo[e];
+                if (gated) {
+                    float g[V];
+                    lds(g, s.g + l * p.C + j * cstep);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        float a, da;
+                        gate_value(p.gate_kind, g[e], a, da);
+                        k[l][j][e] *= a;
+                    }
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < 2 * l + 1; ++m) {
+                float y[V], b[V];
+                lds(y, s.x + (l * l + m) * p.C + j * cstep);
+                if (post) {
+                    lds(b, s.b + (l * l + m) * p.C + j * cstep);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) y[e] += k[l][j][e] * b[e];
+                    if (live) put(static_cast<T*>(p.x_out) + row + (l * l + m) * p.C + c0 + j * cstep, y);
+                }
+#pragma unroll
+                for (int e = 0; e < V; ++e) sy[l] += y[e] * y[e];
+            }
+        }
+    }
+    if (pre) {
+        sum(sy);
+#pragma unroll
+        for (int l = 0; l <= L; ++l) {
+            sy[l] = rsqrtf(sy[l] * (1.f / ((2 * l + 1) * (float)p.C)) + p.eps);
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if (!own[j]) continue;
+                float wi[V];
+                lds(wi, w + (L + 1 + l) * p.C + c0 + j * cstep);
+#pragma unroll
+                for (int m = 0; m < 2 * l + 1; ++m) {
+                    float y[V], b[V];
+                    lds(y, s.x + (l * l + m) * p.C + j * cstep);
+                    if (post) {
+                        lds(b, s.b + (l * l + m) * p.C + j * cstep);
+#pragma unroll
+                        for (int e = 0; e < V; ++e) y[e] += k[l][j][e] * b[e];
+                    }
+#pragma unroll
+                    for (int e = 0; e < V; ++e) y[e] *= sy[l] * wi[e];
+                    if (live) put(static_cast<T*>(p.h) + row + (l * l + m) * p.C + c0 + j * cstep, y);
+                }
+            }
+        }
+    }
+    if (p.stats && lead && live)
+#pragma unroll
+        for (int l = 0; l <= L; ++l) {
+            if (post) p.stats[srow + l] = sb[l];
+            if (pre) p.stats[(int64_t)p.N * (L + 1) + srow + l] = sy[l];
+        }
+    (void)grow;
+}
+
+template <class T, int V, int L, int J>
+__device__ __forceinline__ void bwd_node(const BnParams& p, const View<T>& s, const float* w, const bool (&own)[J],
+                                         int cstep, bool live, int64_t row, int64_t grow, int c0,
+                                         const float (&sb)[L + 1], const float (&sy)[L + 1],
+                                         float (&dwo)[L + 1][J][V], float (&dwi)[L + 1][J][V],
+                                         WorkerSum<L + 1>& sum) {
+    const bool post = p.b != nullptr, pre = p.g_h != nullptr, gated = p.gate != nullptr, more = p.g_x != nullptr;
+    float sa[L + 1][J][V], da[L + 1][J][V];     // scale a(gate), scale a'(gate)
+    float mpy[L + 1], mqb[L + 1];
+    // y of a row: x + k b with k = sa sb w_post
+    const auto y_of = [&](int l, int r, int j, const float (&k)[V], const float (&b)[V], float (&y)[V]) {
+        lds(y, s.x + r * p.C + j * cstep);
+        if (post)
+#pragma unroll
+            for (int e = 0; e < V; ++e) y[e] += k[e] * b[e];
+        (void)l;
+    };
+#pragma unroll
+    for (int l = 0; l <= L; ++l) {
+        mpy[l] = mqb[l] = 0.f;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            if (!own[j]) continue;
+            if (gated) {
+                float g[V];
+                lds(g, s.g + l * p.C + j * cstep);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    gate_value(p.gate_kind, g[e], sa[l][j][e], da[l][j][e]);
+                    sa[l][j][e] *= p.scale;
+                    da[l][j][e] *= p.scale;
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    sa[l][j][e] = p.scale;
+                    da[l][j][e] = 0.f;
+                }
+            }
+            if (!pre) continue;
+            float wi[V], k[V], b[V];
+            lds(wi, w + (L + 1 + l) * p.C + c0 + j * cstep);
+            if (post) {
+                lds(k, w + l * p.C + c0 + j * cstep);
+#pragma unroll
+                for (int e = 0; e < V; ++e) k[e] *= sa[l][j][e] * sb[l];
+            }
+#pragma unroll
+            for (int m = 0; m < 2 * l + 1; ++m) {
+                float gh[V], y[V];
+                if (post) lds(b, s.b + (l * l + m) * p.C + j * cstep);
+                y_of(l, l * l + m, j, k, b, y);
+                lds(gh, s.gh + (l * l + m) * p.C + j * cstep);
+#pragma unroll
+                for (int e = 0; e < V; ++e) mpy[l] += gh[e] * wi[e] * y[e];
+            }
+        }
+    }
+    if (pre) {
+        sum(mpy);
+#pragma unroll
+        for (int l = 0; l <= L; ++l) mpy[l] *= sy[l] * sy[l] * (1.f / ((2 * l + 1) * (float)p.C));
+    }
+#pragma unroll
+    for (int l = 0; l <= L; ++l)
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            if (!own[j]) continue;
+            float wi[V], wo[V], k[V], tb[V], gy[V];
+            if (pre) lds(wi, w + (L + 1 + l) * p.C + c0 + j * cstep);
+            if (post) lds(wo, w + l * p.C + c0 + j * cstep);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                tb[e] = gy[e] = 0.f;
+                k[e] = post ? wo[e] * sa[l][j][e] * sb[l] : 0.f;
+            }
+#pragma unroll
+            for (int m = 0; m < 2 * l + 1; ++m) {
+                const int r = l * l + m;
+                float t[V], b[V];
+                if (post) lds(b, s.b + r * p.C + j * cstep);
+                if (more) lds(t, s.gx + r * p.C + j * cstep);
+                else
+#pragma unroll
+                    for (int e = 0; e < V; ++e) t[e] = 0.f;
+                if (pre) {
+                    float gh[V], y[V];
+                    y_of(l, r, j, k, b, y);
+                    lds(gh, s.gh + r * p.C + j * cstep);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        t[e] += sy[l] * (gh[e] * wi[e] - y[e] * mpy[l]);
+                        gy[e] += gh[e] * y[e];
+                    }
+                }
+                if (post)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) tb[e] += t[e] * b[e];
+                if (live) put(static_cast<T*>(p.dx) + row + r * p.C + c0 + j * cstep, t);
+            }
+            float dg[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                if (post) {
+                    const float u = sa[l][j][e] * tb[e];
+                    mqb[l] += u * wo[e];
+                    if (live) dwo[l][j][e] += u * sb[l];
+                    dg[e] = da[l][j][e] * sb[l] * wo[e] * tb[e];
+                }
+                if (live && pre) dwi[l][j][e] += sy[l] * gy[e];
+            }
+            if (gated && live) put(static_cast<T*>(p.dgate) + grow + l * p.C + c0 + j * cstep, dg);
+        }
+    if (!post) return;
+    sum(mqb);
+#pragma unroll
+    for (int l = 0; l <= L; ++l) {
+        mqb[l] *= sb[l] * sb[l] * (1.f / ((2 * l + 1) * (float)p.C));
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            if (!own[j]) continue;
+            float wi[V], wo[V], k[V];
+            if (pre) lds(wi, w + (L + 1 + l) * p.C + c0 + j * cstep);
+            lds(wo, w + l * p.C + c0 + j * cstep);
+#pragma unroll
+            for (int e = 0; e < V; ++e) k[e] = wo[e] * sa[l][j][e] * sb[l];
+#pragma unroll
+            for (int m = 0; m < 2 * l + 1; ++m) {
+                const int r = l * l + m;
+                float t[V], b[V];
+                lds(b, s.b + r * p.C + j * cstep);
+                if (more) lds(t, s.gx + r * p.C + j * cstep);
+                else
+#pragma unroll
+                    for (int e = 0; e < V; ++e) t[e] = 0.f;
+                if (pre) {
+                    float gh[V], y[V];
+                    y_of(l, r, j, k, b, y);
+                    lds(gh, s.gh + r * p.C + j * cstep);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) t[e] += sy[l] * (gh[e] * wi[e] - y[e] * mpy[l]);
+                }
+#pragma unroll
+                for (int e = 0; e < V; ++e) t[e] = k[e] * t[e] - sb[l] * b[e] * mqb[l];
+                if (live) put(static_cast<T*>(p.db) + row + r * p.C + c0 + j * cstep, t);
+            }
+        }
+    }
+}
+
+// Shared memory: [w_post, w_pre: 2 (L + 1) C floats] [ring of slots].
+template <class T, int V, int L, int J, bool BWD, bool CTA>
+__global__ void __launch_bounds__(256, (CTA && J * V <= 16 && L == 0) ? 2 : 1) bn_staged_kernel(const StagedParams s) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ uint64_t full[kMaxSlots];
+    __shared__ float red[2 * (L + 1) * 16];
+    constexpr int D = (L + 1) * (L + 1);
+    const BnParams& p = s.p;
+    float* w = reinterpret_cast<float*>(smem);
+    const Ring ring{smem + 2 * (L + 1) * p.C * sizeof(float), full};
+    const int workers = CTA ? 1 : blockDim.x / 32, worker = CTA ? 0 : threadIdx.x / 32;
+    const int lane = CTA ? threadIdx.x : threadIdx.x & 31;
+    const int width = CTA ? (int)blockDim.x : p.width;
+    const int sub = CTA ? 0 : lane / width, x0 = lane - sub * width;
+    const int c0 = x0 * V, cstep = width * V;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < s.slots; ++i) bulk::init(full + i);
+        bulk::fence_init();
+    }
+    for (int i = threadIdx.x; i < (L + 1) * p.C; i += blockDim.x) {
+        w[i] = p.w_post ? p.w_post[i] : 0.f;
+        w[(L + 1) * p.C + i] = p.w_pre ? p.w_pre[i] : 0.f;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0)
+        for (int k = 0; k < s.slots; ++k) fill<BWD>(s, ring, k);
+    bool own[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) own[j] = c0 + j * cstep < p.C;
+    float dwo[BWD ? L + 1 : 1][J][V], dwi[BWD ? L + 1 : 1][J][V];
+#pragma unroll
+    for (int l = 0; l < (BWD ? L + 1 : 1); ++l)
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int e = 0; e < V; ++e) dwo[l][j][e] = dwi[l][j][e] = 0.f;
+    WorkerSum<L + 1> sum{red, width, 0};
+    const int mine = s.total > blockIdx.x ? (int)((s.total - blockIdx.x + gridDim.x - 1) / gridDim.x) : 0;
+    bool ok = true;
+    for (int k = worker; k < mine; k += workers) {
+        const int slot = k % s.slots;
+        const int64_t n = (blockIdx.x + (int64_t)k * gridDim.x) * s.nodes + sub;
+        const bool live = n < p.N;
+        float sb[L + 1], sy[L + 1];
+        if constexpr (BWD) {
+#pragma unroll
+            for (int l = 0; l <= L; ++l) {
+                sb[l] = live && p.b ? __ldg(p.stats + n * (L + 1) + l) : 0.f;
+                sy[l] = live && p.g_h ? __ldg(p.stats + ((int64_t)p.N + n) * (L + 1) + l) : 0.f;
+            }
+        }
+        if (!bulk::wait(full + slot, (uint32_t)(k / s.slots) & 1u)) {
+            atomicOr(s.status, 4u);
+            ok = false;
+            break;
+        }
+        const unsigned char* base = ring.base + (int64_t)slot * s.slot_bytes;
+        const auto at = [&](int o, int bytes) {
+            return reinterpret_cast<const T*>(base + o + sub * bytes) + c0;
+        };
+        const View<T> v{at(s.o_x, s.node_bytes), at(s.o_b, s.node_bytes), at(s.o_gx, s.node_bytes),
+                        at(s.o_gh, s.node_bytes), at(s.o_g, s.gate_bytes)};
+        const int64_t row = n * D * p.C, grow = n * (L + 1) * p.C;
+        if constexpr (BWD)
+            bwd_node<T, V, L, J>(p, v, w, own, cstep, live, row, grow, c0, sb, sy, dwo, dwi, sum);
+        else
+            fwd_node<T, V, L, J>(p, v, w, own, cstep, live, row, grow, n * (L + 1), c0, x0 == 0, sum);
+        // everyone has read the slot: its next copies may come
+        if constexpr (CTA) __syncthreads();
+        else __syncwarp();
+        if (lane == 0) fill<BWD>(s, ring, k + s.slots);
+    }
+    if (!ok) {
+        // the copies still in flight end before the CTA's memory does (each wait is bounded)
+        if (lane == 0)
+            for (int i = 0; i < s.slots; ++i) bulk::wait(full + i, 0), bulk::wait(full + i, 1);
+        return;
+    }
+    if constexpr (BWD) {
+        float* part = p.part + (int64_t)blockIdx.x * 2 * (L + 1) * p.C;
+        if constexpr (CTA) {
+#pragma unroll
+            for (int l = 0; l <= L; ++l)
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+                    if (own[j])
+#pragma unroll
+                        for (int e = 0; e < V; ++e) {
+                            part[l * p.C + c0 + j * cstep + e] = dwo[l][j][e];
+                            part[(L + 1 + l) * p.C + c0 + j * cstep + e] = dwi[l][j][e];
+                        }
+        } else {
+            // the warps' sums in order, and within a warp its nodes', one degree and kind at a time
+            __syncthreads();      // every slot has been read
+            float* t = reinterpret_cast<float*>(smem + 2 * (L + 1) * p.C * sizeof(float));
+#pragma unroll
+            for (int l = 0; l <= L; ++l)
+#pragma unroll
+                for (int which = 0; which < 2; ++which) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        t[threadIdx.x * V + e] = which ? dwi[l][0][e] : dwo[l][0][e];
+                    __syncthreads();
+                    const int groups = workers * (32 / width);
+                    for (int c = threadIdx.x; c < p.C; c += blockDim.x) {
+                        float v = 0.f;
+                        for (int g = 0; g < groups; ++g) v += t[(g * width) * V + c];
+                        part[(which * (L + 1) + l) * p.C + c] = v;
+                    }
+                    __syncthreads();
+                }
+        }
+    }
+}
+
+// How a staged launch is cut; slots 0: not staged.
+struct Staged {
+    int V, J, width, threads, slots, nodes, ctas, smem;
+};
+
+// Two slots at least, of what an SM's shared memory holds; workers that leave
+// two fifths of the slots to the copies in flight.
+inline Staged staged_shape(int L, int C, int es, int tensors, bool gated) {
+    Staged s{};
+    const int room = 224 * 1024, wbytes = 2 * (L + 1) * C * 4;
+    const int64_t node = (int64_t)(L + 1) * (L + 1) * C * es * tensors + (gated ? (int64_t)(L + 1) * C * es : 0);
+    if ((int64_t)C * es % 16 != 0) return s;
+    s.V = L == 0 ? 16 / es : 4;
+    s.J = 1;
+    const int vecs = C / s.V;
+    if (vecs <= 32) {
+        s.width = 1;
+        while (s.width < vecs) s.width *= 2;
+        s.nodes = 32 / s.width;
+        s.ctas = 1;
+        const int64_t fit = (room - wbytes) / (node * s.nodes);
+        s.slots = (int)(fit < kMaxSlots ? fit : kMaxSlots);
+        if (s.slots < 2) return Staged{};
+        int warps = s.slots * 3 / 5;
+        warps = warps < 1 ? 1 : warps > 8 ? 8 : warps;
+        s.threads = 32 * warps;
+        // the reduction of the weight gradients takes threads * V floats of the ring
+        if ((int64_t)s.slots * s.nodes * node < (int64_t)s.threads * s.V * 4) return Staged{};
+    } else {
+        while (s.J < (L == 0 ? 4 : 1) && (vecs + s.J - 1) / s.J > 256) s.J *= 2;
+        const int across = (vecs + s.J - 1) / s.J;
+        if (across > 256) return Staged{};
+        s.width = s.threads = (across + 31) / 32 * 32;
+        s.nodes = 1;
+        s.ctas = L == 0 && s.J * s.V <= 16 && 2 * (wbytes + 2 * node) <= room ? 2 : 1;
+        const int64_t fit = (room / s.ctas - wbytes) / node;
+        s.slots = (int)(fit < kMaxSlots ? fit : kMaxSlots);
+        if (s.slots < 2) return Staged{};
+    }
+    s.smem = wbytes + (int)(node * s.nodes) * s.slots;
+    return s;
+}
+
+template <class T, int V, int L, int J, bool BWD, bool CTA>
+cudaError_t launch_staged(const StagedParams& s, const Staged& h, int grid, cudaStream_t st) {
+    static bool done[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !done[dev]) {
+        e = cudaFuncSetAttribute(bn_staged_kernel<T, V, L, J, BWD, CTA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 225 * 1024);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) done[dev] = true;
+    }
+    bn_staged_kernel<T, V, L, J, BWD, CTA><<<grid, h.threads, h.smem, st>>>(s);
+    count_launch();
+    return cudaGetLastError();
+}
+
+template <class T, bool BWD>
+cudaError_t staged_for(const StagedParams& s, const Staged& h, int grid, cudaStream_t st) {
+    constexpr int W = 16 / sizeof(T);
+    const bool cta = h.width > 32;
+    switch (s.p.L) {
+        case 0:
+            if (!cta) return launch_staged<T, W, 0, 1, BWD, false>(s, h, grid, st);
+            if (h.J == 1) return launch_staged<T, W, 0, 1, BWD, true>(s, h, grid, st);
+            if (h.J == 2) return launch_staged<T, W, 0, 2, BWD, true>(s, h, grid, st);
+            return launch_staged<T, W, 0, 4, BWD, true>(s, h, grid, st);
+        case 1:
+            return cta ? launch_staged<T, 4, 1, 1, BWD, true>(s, h, grid, st)
+                       : launch_staged<T, 4, 1, 1, BWD, false>(s, h, grid, st);
+        case 2:
+            return cta ? launch_staged<T, 4, 2, 1, BWD, true>(s, h, grid, st)
+                       : launch_staged<T, 4, 2, 1, BWD, false>(s, h, grid, st);
+        default:
+            return cta ? launch_staged<T, 4, 3, 1, BWD, true>(s, h, grid, st)
+                       : launch_staged<T, 4, 3, 1, BWD, false>(s, h, grid, st);
+    }
+}
+
+}  // namespace bn
+}  // namespace eqc

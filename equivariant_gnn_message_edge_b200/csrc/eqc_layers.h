@@ -36,6 +36,7 @@ struct BlockNormArgs {
     void *dx, *db, *dgate;
     float *dw_post, *dw_pre;
     float* part;
+    unsigned* status;
 };
 cudaError_t block_norm_forward(const BlockNormArgs& a, cudaStream_t st);
 size_t block_norm_workspace(int L, int C, int N);

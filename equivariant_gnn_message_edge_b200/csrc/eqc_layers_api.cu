@@ -111,6 +111,7 @@ int norm_args(eqconv_plan_t plan, int N, const void* x, const void* b, const voi
     a.gate = gate;
     a.w_post = w_post;
     a.w_pre = w_pre;
+    a.status = plan->d_status;
     return EQCONV_OK;
 }
 
