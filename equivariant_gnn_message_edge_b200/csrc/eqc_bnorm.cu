@@ -83,7 +83,7 @@ Staged staged_for_args(const BlockNormArgs& a, bool bwd) {
         all |= reinterpret_cast<uintptr_t>(q);
     if (all % 16 != 0) return Staged{};
     const int tensors = bwd ? 2 * (a.g_h != nullptr) + (a.b != nullptr) + (a.g_x != nullptr) : 1 + (a.b != nullptr);
-    return tensors ? staged_shape(a.L, a.C, type_bytes(a.type), tensors, a.gate != nullptr) : Staged{};
+    return tensors ? staged_shape(a.L, a.C, type_bytes(a.type), tensors, a.gate != nullptr, bwd) : Staged{};
 }
 
 // rows: of the partial sums a CTA leaves (see bn_dw_reduce).
@@ -152,8 +152,8 @@ size_t block_norm_workspace(int L, int C, int N) {
     }
     int64_t ctas = (int64_t)bn::kSMs * most;
     if (ctas > (int64_t)N * (L + 1)) ctas = (int64_t)N * (L + 1);
-    // or two CTAs an SM with the sums of all degrees
-    int64_t staged = 2 * (int64_t)bn::kSMs;
+    // or, with the sums of all degrees, two CTAs an SM (more for wide rows that need less than an SM's threads)
+    int64_t staged = (int64_t)bn::kSMs * (L == 0 && C < 2048 ? 16 : 2);
     if (staged > N) staged = N;
     const int64_t r = ctas + L + 1 > staged * (L + 1) ? ctas + L + 1 : staged * (L + 1);
     return (size_t)r * 2 * C * sizeof(float);

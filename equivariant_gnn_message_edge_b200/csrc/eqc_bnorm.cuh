@@ -48,16 +48,51 @@ struct BnParams {
     int width;           // threads across the channels of a group (a power of two up to 32, or whole warps)
 };
 
-// a(g) and a'(g) of the gate kinds (EQCONV_GATE_*).
-__device__ __forceinline__ void gate_value(int kind, float g, float& a, float& da) {
+// a(g) and a'(g) of V gates, of one kind (EQCONV_GATE_*).  exp and 1/x are the
+// hardware's approximations: a few units in the last place of fp32, and |g|
+// more of them through exp's argument.  tanh is (1 - q) / (1 + q) of
+// q = exp(-2 |g|), and near 0, where that cancels, its Taylor series (for
+// |g| < 0.25 the first term left out is below 2^-28 of the value).
+template <int V>
+__device__ __forceinline__ void gate_values(int kind, const float (&g)[V], float (&a)[V], float (&da)[V]) {
     if (kind == 3) {
-        a = tanhf(g);
-        da = 1.f - a * a;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float q = __expf(-2.f * fabsf(g[e])), g2 = g[e] * g[e];
+            const float far = copysignf(__fdividef(1.f - q, 1.f + q), g[e]);
+            float c = fmaf(g2, -1382.f / 155925.f, 62.f / 2835.f);
+            c = fmaf(g2, c, -17.f / 315.f);
+            c = fmaf(g2, c, 2.f / 15.f);
+            c = fmaf(g2, c, -1.f / 3.f);
+            const float near = fmaf(g[e] * g2, c, g[e]);
+            a[e] = g2 < 0.0625f ? near : far;
+            da[e] = fmaf(-a[e], a[e], 1.f);
+        }
     } else {
-        const float s = 1.f / (1.f + expf(-g));
-        a = kind == 1 ? s : g * s;
-        da = kind == 1 ? s * (1.f - s) : s * (1.f + g * (1.f - s));
+        float s[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) s[e] = __fdividef(1.f, 1.f + __expf(-g[e]));
+        if (kind == 1) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                a[e] = s[e];
+                da[e] = s[e] * (1.f - s[e]);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                a[e] = g[e] * s[e];
+                da[e] = s[e] * fmaf(g[e], 1.f - s[e], 1.f);
+            }
+        }
     }
+}
+
+__device__ __forceinline__ void gate_value(int kind, float g, float& a, float& da) {
+    float gv[1] = {g}, av[1], dv[1];
+    gate_values(kind, gv, av, dv);
+    a = av[0];
+    da = dv[0];
 }
 
 __device__ __forceinline__ float block_sum(float v, float* red) {
@@ -218,7 +253,6 @@ struct WorkerSum {
 #pragma unroll
                 for (int i = 0; i < NB; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
         if (width <= 32) return;
-        const int warps = width >> 5;
         float* r = red + flip * NB * 16;
         flip ^= 1;       // the next sum's buffer: one barrier a sum is enough
         if ((threadIdx.x & 31) == 0)
@@ -227,6 +261,7 @@ struct WorkerSum {
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
+            const int warps = width >> 5;
             float s = 0.f;
             for (int w = 0; w < warps; ++w) s += r[i * 16 + w];
             v[i] = s;
@@ -306,12 +341,16 @@ __device__ __forceinline__ void fwd_groups(const BnParams& p, int l, float* red)
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 if (!own[j] || nw + i >= p.N) continue;
+                float a[V], da[V];
+                if (gated) {
+                    float gv[V];
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    float a = 1.f, da;
-                    if (gated) gate_value(p.gate_kind, g[i][j].get(e), a, da);
-                    k[i][j][e] = post ? p.scale * a * sb[i] * wo[j].e[e] : 0.f;
+                    for (int e = 0; e < V; ++e) gv[e] = g[i][j].get(e);
+                    gate_values(p.gate_kind, gv, a, da);
                 }
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    k[i][j][e] = post ? p.scale * (gated ? a[e] : 1.f) * sb[i] * wo[j].e[e] : 0.f;
 #pragma unroll
                 for (int m = 0; m < K; ++m) {
                     Pack<T, V> o;
@@ -415,12 +454,16 @@ __device__ __forceinline__ void bwd_groups(const BnParams& p, int l, float* red,
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 if (!own[j] || nw + i >= p.N) continue;
+                if (gated) {
+                    float gv[V];
+#pragma unroll
+                    for (int e = 0; e < V; ++e) gv[e] = g[i][j].get(e);
+                    gate_values(p.gate_kind, gv, sa[i][j], da[i][j]);
+                }
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    float a = 1.f, d = 0.f;
-                    if (gated) gate_value(p.gate_kind, g[i][j].get(e), a, d);
-                    sa[i][j][e] = p.scale * a;
-                    da[i][j][e] = p.scale * d;
+                    sa[i][j][e] = gated ? p.scale * sa[i][j][e] : p.scale;
+                    da[i][j][e] = gated ? p.scale * da[i][j][e] : 0.f;
                 }
                 if (pre)
 #pragma unroll

@@ -8,7 +8,7 @@
 //
 // A worker is a warp (32 / width nodes a slot, several workers share the ring)
 // or, for wide nodes, the whole CTA (one node a slot).  Its threads own V
-// neighbouring channels, J times, of every row of the node.
+// neighbouring channels of every row of the node.
 #pragma once
 
 #include "eqc_bnorm.cuh"
@@ -81,10 +81,9 @@ __device__ __forceinline__ void put(T* p, const float (&v)[V]) {
     o.store(p);
 }
 
-template <class T, int V, int L, int J>
-__device__ __forceinline__ void fwd_node(const BnParams& p, const View<T>& s, const float* w, const bool (&own)[J],
-                                         int cstep, bool live, int64_t row, int64_t grow, int64_t srow, int c0,
-                                         bool lead, WorkerSum<L + 1>& sum) {
+template <class T, int V, int L>
+__device__ __forceinline__ void fwd_node(const BnParams& p, const View<T>& s, const float* w, bool own, bool live,
+                                         int64_t row, int64_t srow, int c0, bool lead, WorkerSum<L + 1>& sum) {
     const bool post = p.b != nullptr, pre = p.w_pre != nullptr, gated = p.gate != nullptr;
     float sb[L + 1], sy[L + 1];
 #pragma unroll
@@ -92,50 +91,44 @@ __device__ __forceinline__ void fwd_node(const BnParams& p, const View<T>& s, co
     if (post) {
 #pragma unroll
         for (int l = 0; l <= L; ++l)
+            if (own)
 #pragma unroll
-            for (int j = 0; j < J; ++j)
-                if (own[j])
+                for (int m = 0; m < 2 * l + 1; ++m) {
+                    float b[V];
+                    lds(b, s.b + (l * l + m) * p.C);
 #pragma unroll
-                    for (int m = 0; m < 2 * l + 1; ++m) {
-                        float b[V];
-                        lds(b, s.b + (l * l + m) * p.C + j * cstep);
-#pragma unroll
-                        for (int e = 0; e < V; ++e) sb[l] += b[e] * b[e];
-                    }
+                    for (int e = 0; e < V; ++e) sb[l] += b[e] * b[e];
+                }
         sum(sb);
     }
-    float k[L + 1][J][V];
+    float k[L + 1][V];
 #pragma unroll
     for (int l = 0; l <= L; ++l) {
         if (post) sb[l] = rsqrtf(sb[l] * (1.f / ((2 * l + 1) * (float)p.C)) + p.eps);
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-            if (!own[j]) continue;
+        if (own) {
             if (post) {
                 float wo[V];
-                lds(wo, w + l * p.C + c0 + j * cstep);
+                lds(wo, w + l * p.C + c0);
 #pragma unroll
-                for (int e = 0; e < V; ++e) k[l][j][e] = p.scale * sb[l] * wo[e];
+                for (int e = 0; e < V; ++e) k[l][e] = p.scale * sb[l] * wo[e];
                 if (gated) {
                     float g[V];
-                    lds(g, s.g + l * p.C + j * cstep);
+                    lds(g, s.g + l * p.C);
+                    float a[V], da[V];
+                    gate_values(p.gate_kind, g, a, da);
 #pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        float a, da;
-                        gate_value(p.gate_kind, g[e], a, da);
-                        k[l][j][e] *= a;
-                    }
+                    for (int e = 0; e < V; ++e) k[l][e] *= a[e];
                 }
             }
 #pragma unroll
             for (int m = 0; m < 2 * l + 1; ++m) {
                 float y[V], b[V];
-                lds(y, s.x + (l * l + m) * p.C + j * cstep);
+                lds(y, s.x + (l * l + m) * p.C);
                 if (post) {
-                    lds(b, s.b + (l * l + m) * p.C + j * cstep);
+                    lds(b, s.b + (l * l + m) * p.C);
 #pragma unroll
-                    for (int e = 0; e < V; ++e) y[e] += k[l][j][e] * b[e];
-                    if (live) put(static_cast<T*>(p.x_out) + row + (l * l + m) * p.C + c0 + j * cstep, y);
+                    for (int e = 0; e < V; ++e) y[e] += k[l][e] * b[e];
+                    if (live) put(static_cast<T*>(p.x_out) + row + (l * l + m) * p.C + c0, y);
                 }
 #pragma unroll
                 for (int e = 0; e < V; ++e) sy[l] += y[e] * y[e];
@@ -147,23 +140,21 @@ __device__ __forceinline__ void fwd_node(const BnParams& p, const View<T>& s, co
 #pragma unroll
         for (int l = 0; l <= L; ++l) {
             sy[l] = rsqrtf(sy[l] * (1.f / ((2 * l + 1) * (float)p.C)) + p.eps);
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-                if (!own[j]) continue;
+            if (own) {
                 float wi[V];
-                lds(wi, w + (L + 1 + l) * p.C + c0 + j * cstep);
+                lds(wi, w + (L + 1 + l) * p.C + c0);
 #pragma unroll
                 for (int m = 0; m < 2 * l + 1; ++m) {
                     float y[V], b[V];
-                    lds(y, s.x + (l * l + m) * p.C + j * cstep);
+                    lds(y, s.x + (l * l + m) * p.C);
                     if (post) {
-                        lds(b, s.b + (l * l + m) * p.C + j * cstep);
+                        lds(b, s.b + (l * l + m) * p.C);
 #pragma unroll
-                        for (int e = 0; e < V; ++e) y[e] += k[l][j][e] * b[e];
+                        for (int e = 0; e < V; ++e) y[e] += k[l][e] * b[e];
                     }
 #pragma unroll
                     for (int e = 0; e < V; ++e) y[e] *= sy[l] * wi[e];
-                    if (live) put(static_cast<T*>(p.h) + row + (l * l + m) * p.C + c0 + j * cstep, y);
+                    if (live) put(static_cast<T*>(p.h) + row + (l * l + m) * p.C + c0, y);
                 }
             }
         }
@@ -174,62 +165,57 @@ __device__ __forceinline__ void fwd_node(const BnParams& p, const View<T>& s, co
             if (post) p.stats[srow + l] = sb[l];
             if (pre) p.stats[(int64_t)p.N * (L + 1) + srow + l] = sy[l];
         }
-    (void)grow;
 }
 
-template <class T, int V, int L, int J>
-__device__ __forceinline__ void bwd_node(const BnParams& p, const View<T>& s, const float* w, const bool (&own)[J],
-                                         int cstep, bool live, int64_t row, int64_t grow, int c0,
-                                         const float (&sb)[L + 1], const float (&sy)[L + 1],
-                                         float (&dwo)[L + 1][J][V], float (&dwi)[L + 1][J][V],
+template <class T, int V, int L>
+__device__ __forceinline__ void bwd_node(const BnParams& p, const View<T>& s, const float* w, bool own, bool live,
+                                         int64_t row, int64_t grow, int c0, const float (&sb)[L + 1],
+                                         const float (&sy)[L + 1], float (&dwo)[L + 1][V], float (&dwi)[L + 1][V],
                                          WorkerSum<L + 1>& sum) {
     const bool post = p.b != nullptr, pre = p.g_h != nullptr, gated = p.gate != nullptr, more = p.g_x != nullptr;
-    float sa[L + 1][J][V], da[L + 1][J][V];     // scale a(gate), scale a'(gate)
+    float sa[L + 1][V], da[L + 1][V];     // scale a(gate), scale a'(gate)
     float mpy[L + 1], mqb[L + 1];
     // y of a row: x + k b with k = sa sb w_post
-    const auto y_of = [&](int l, int r, int j, const float (&k)[V], const float (&b)[V], float (&y)[V]) {
-        lds(y, s.x + r * p.C + j * cstep);
+    const auto y_of = [&](int r, const float (&k)[V], const float (&b)[V], float (&y)[V]) {
+        lds(y, s.x + r * p.C);
         if (post)
 #pragma unroll
             for (int e = 0; e < V; ++e) y[e] += k[e] * b[e];
-        (void)l;
     };
 #pragma unroll
     for (int l = 0; l <= L; ++l) {
         mpy[l] = mqb[l] = 0.f;
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-            if (!own[j]) continue;
+        if (own) {
             if (gated) {
                 float g[V];
-                lds(g, s.g + l * p.C + j * cstep);
+                lds(g, s.g + l * p.C);
+                gate_values(p.gate_kind, g, sa[l], da[l]);
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    gate_value(p.gate_kind, g[e], sa[l][j][e], da[l][j][e]);
-                    sa[l][j][e] *= p.scale;
-                    da[l][j][e] *= p.scale;
+                    sa[l][e] *= p.scale;
+                    da[l][e] *= p.scale;
                 }
             } else {
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    sa[l][j][e] = p.scale;
-                    da[l][j][e] = 0.f;
+                    sa[l][e] = p.scale;
+                    da[l][e] = 0.f;
                 }
             }
             if (!pre) continue;
             float wi[V], k[V], b[V];
-            lds(wi, w + (L + 1 + l) * p.C + c0 + j * cstep);
+            lds(wi, w + (L + 1 + l) * p.C + c0);
             if (post) {
-                lds(k, w + l * p.C + c0 + j * cstep);
+                lds(k, w + l * p.C + c0);
 #pragma unroll
-                for (int e = 0; e < V; ++e) k[e] *= sa[l][j][e] * sb[l];
+                for (int e = 0; e < V; ++e) k[e] *= sa[l][e] * sb[l];
             }
 #pragma unroll
             for (int m = 0; m < 2 * l + 1; ++m) {
                 float gh[V], y[V];
-                if (post) lds(b, s.b + (l * l + m) * p.C + j * cstep);
-                y_of(l, l * l + m, j, k, b, y);
-                lds(gh, s.gh + (l * l + m) * p.C + j * cstep);
+                if (post) lds(b, s.b + (l * l + m) * p.C);
+                y_of(l * l + m, k, b, y);
+                lds(gh, s.gh + (l * l + m) * p.C);
 #pragma unroll
                 for (int e = 0; e < V; ++e) mpy[l] += gh[e] * wi[e] * y[e];
             }
@@ -242,30 +228,28 @@ __device__ __forceinline__ void bwd_node(const BnParams& p, const View<T>& s, co
     }
 #pragma unroll
     for (int l = 0; l <= L; ++l)
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-            if (!own[j]) continue;
+        if (own) {
             float wi[V], wo[V], k[V], tb[V], gy[V];
-            if (pre) lds(wi, w + (L + 1 + l) * p.C + c0 + j * cstep);
-            if (post) lds(wo, w + l * p.C + c0 + j * cstep);
+            if (pre) lds(wi, w + (L + 1 + l) * p.C + c0);
+            if (post) lds(wo, w + l * p.C + c0);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 tb[e] = gy[e] = 0.f;
-                k[e] = post ? wo[e] * sa[l][j][e] * sb[l] : 0.f;
+                k[e] = post ? wo[e] * sa[l][e] * sb[l] : 0.f;
             }
 #pragma unroll
             for (int m = 0; m < 2 * l + 1; ++m) {
                 const int r = l * l + m;
                 float t[V], b[V];
-                if (post) lds(b, s.b + r * p.C + j * cstep);
-                if (more) lds(t, s.gx + r * p.C + j * cstep);
+                if (post) lds(b, s.b + r * p.C);
+                if (more) lds(t, s.gx + r * p.C);
                 else
 #pragma unroll
                     for (int e = 0; e < V; ++e) t[e] = 0.f;
                 if (pre) {
                     float gh[V], y[V];
-                    y_of(l, r, j, k, b, y);
-                    lds(gh, s.gh + r * p.C + j * cstep);
+                    y_of(r, k, b, y);
+                    lds(gh, s.gh + r * p.C);
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
                         t[e] += sy[l] * (gh[e] * wi[e] - y[e] * mpy[l]);
@@ -275,61 +259,59 @@ __device__ __forceinline__ void bwd_node(const BnParams& p, const View<T>& s, co
                 if (post)
 #pragma unroll
                     for (int e = 0; e < V; ++e) tb[e] += t[e] * b[e];
-                if (live) put(static_cast<T*>(p.dx) + row + r * p.C + c0 + j * cstep, t);
+                if (live) put(static_cast<T*>(p.dx) + row + r * p.C + c0, t);
             }
             float dg[V];
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 if (post) {
-                    const float u = sa[l][j][e] * tb[e];
+                    const float u = sa[l][e] * tb[e];
                     mqb[l] += u * wo[e];
-                    if (live) dwo[l][j][e] += u * sb[l];
-                    dg[e] = da[l][j][e] * sb[l] * wo[e] * tb[e];
+                    if (live) dwo[l][e] += u * sb[l];
+                    dg[e] = da[l][e] * sb[l] * wo[e] * tb[e];
                 }
-                if (live && pre) dwi[l][j][e] += sy[l] * gy[e];
+                if (live && pre) dwi[l][e] += sy[l] * gy[e];
             }
-            if (gated && live) put(static_cast<T*>(p.dgate) + grow + l * p.C + c0 + j * cstep, dg);
+            if (gated && live) put(static_cast<T*>(p.dgate) + grow + l * p.C + c0, dg);
         }
     if (!post) return;
     sum(mqb);
 #pragma unroll
     for (int l = 0; l <= L; ++l) {
         mqb[l] *= sb[l] * sb[l] * (1.f / ((2 * l + 1) * (float)p.C));
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-            if (!own[j]) continue;
+        if (own) {
             float wi[V], wo[V], k[V];
-            if (pre) lds(wi, w + (L + 1 + l) * p.C + c0 + j * cstep);
-            lds(wo, w + l * p.C + c0 + j * cstep);
+            if (pre) lds(wi, w + (L + 1 + l) * p.C + c0);
+            lds(wo, w + l * p.C + c0);
 #pragma unroll
-            for (int e = 0; e < V; ++e) k[e] = wo[e] * sa[l][j][e] * sb[l];
+            for (int e = 0; e < V; ++e) k[e] = wo[e] * sa[l][e] * sb[l];
 #pragma unroll
             for (int m = 0; m < 2 * l + 1; ++m) {
                 const int r = l * l + m;
                 float t[V], b[V];
-                lds(b, s.b + r * p.C + j * cstep);
-                if (more) lds(t, s.gx + r * p.C + j * cstep);
+                lds(b, s.b + r * p.C);
+                if (more) lds(t, s.gx + r * p.C);
                 else
 #pragma unroll
                     for (int e = 0; e < V; ++e) t[e] = 0.f;
                 if (pre) {
                     float gh[V], y[V];
-                    y_of(l, r, j, k, b, y);
-                    lds(gh, s.gh + r * p.C + j * cstep);
+                    y_of(r, k, b, y);
+                    lds(gh, s.gh + r * p.C);
 #pragma unroll
                     for (int e = 0; e < V; ++e) t[e] += sy[l] * (gh[e] * wi[e] - y[e] * mpy[l]);
                 }
 #pragma unroll
                 for (int e = 0; e < V; ++e) t[e] = k[e] * t[e] - sb[l] * b[e] * mqb[l];
-                if (live) put(static_cast<T*>(p.db) + row + r * p.C + c0 + j * cstep, t);
+                if (live) put(static_cast<T*>(p.db) + row + r * p.C + c0, t);
             }
         }
     }
 }
 
 // Shared memory: [w_post, w_pre: 2 (L + 1) C floats] [ring of slots].
-template <class T, int V, int L, int J, bool BWD, bool CTA>
-__global__ void __launch_bounds__(256, (CTA && J * V <= 16 && L == 0) ? 2 : 1) bn_staged_kernel(const StagedParams s) {
+template <class T, int V, int L, bool BWD, bool CTA>
+__global__ void __launch_bounds__(256, 1) bn_staged_kernel(const StagedParams s) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ uint64_t full[kMaxSlots];
     __shared__ float red[2 * (L + 1) * 16];
@@ -341,7 +323,7 @@ __global__ void __launch_bounds__(256, (CTA && J * V <= 16 && L == 0) ? 2 : 1) b
     const int lane = CTA ? threadIdx.x : threadIdx.x & 31;
     const int width = CTA ? (int)blockDim.x : p.width;
     const int sub = CTA ? 0 : lane / width, x0 = lane - sub * width;
-    const int c0 = x0 * V, cstep = width * V;
+    const int c0 = x0 * V;
     if (threadIdx.x == 0) {
         for (int i = 0; i < s.slots; ++i) bulk::init(full + i);
         bulk::fence_init();
@@ -353,16 +335,12 @@ __global__ void __launch_bounds__(256, (CTA && J * V <= 16 && L == 0) ? 2 : 1) b
     __syncthreads();
     if (threadIdx.x == 0)
         for (int k = 0; k < s.slots; ++k) fill<BWD>(s, ring, k);
-    bool own[J];
-#pragma unroll
-    for (int j = 0; j < J; ++j) own[j] = c0 + j * cstep < p.C;
-    float dwo[BWD ? L + 1 : 1][J][V], dwi[BWD ? L + 1 : 1][J][V];
+    const bool own = c0 < p.C;
+    float dwo[BWD ? L + 1 : 1][V], dwi[BWD ? L + 1 : 1][V];
 #pragma unroll
     for (int l = 0; l < (BWD ? L + 1 : 1); ++l)
 #pragma unroll
-        for (int j = 0; j < J; ++j)
-#pragma unroll
-            for (int e = 0; e < V; ++e) dwo[l][j][e] = dwi[l][j][e] = 0.f;
+        for (int e = 0; e < V; ++e) dwo[l][e] = dwi[l][e] = 0.f;
     WorkerSum<L + 1> sum{red, width, 0};
     const int mine = s.total > blockIdx.x ? (int)((s.total - blockIdx.x + gridDim.x - 1) / gridDim.x) : 0;
     bool ok = true;
@@ -391,9 +369,9 @@ __global__ void __launch_bounds__(256, (CTA && J * V <= 16 && L == 0) ? 2 : 1) b
                         at(s.o_gh, s.node_bytes), at(s.o_g, s.gate_bytes)};
         const int64_t row = n * D * p.C, grow = n * (L + 1) * p.C;
         if constexpr (BWD)
-            bwd_node<T, V, L, J>(p, v, w, own, cstep, live, row, grow, c0, sb, sy, dwo, dwi, sum);
+            bwd_node<T, V, L>(p, v, w, own, live, row, grow, c0, sb, sy, dwo, dwi, sum);
         else
-            fwd_node<T, V, L, J>(p, v, w, own, cstep, live, row, grow, n * (L + 1), c0, x0 == 0, sum);
+            fwd_node<T, V, L>(p, v, w, own, live, row, n * (L + 1), c0, x0 == 0, sum);
         // everyone has read the slot: its next copies may come
         if constexpr (CTA) __syncthreads();
         else __syncwarp();
@@ -410,14 +388,10 @@ __global__ void __launch_bounds__(256, (CTA && J * V <= 16 && L == 0) ? 2 : 1) b
         if constexpr (CTA) {
 #pragma unroll
             for (int l = 0; l <= L; ++l)
-#pragma unroll
-                for (int j = 0; j < J; ++j)
-                    if (own[j])
-#pragma unroll
-                        for (int e = 0; e < V; ++e) {
-                            part[l * p.C + c0 + j * cstep + e] = dwo[l][j][e];
-                            part[(L + 1 + l) * p.C + c0 + j * cstep + e] = dwi[l][j][e];
-                        }
+                if (own) {
+                    put(part + l * p.C + c0, dwo[l]);
+                    put(part + (L + 1 + l) * p.C + c0, dwi[l]);
+                }
         } else {
             // the warps' sums in order, and within a warp its nodes', one degree and kind at a time
             __syncthreads();      // every slot has been read
@@ -428,7 +402,7 @@ __global__ void __launch_bounds__(256, (CTA && J * V <= 16 && L == 0) ? 2 : 1) b
                 for (int which = 0; which < 2; ++which) {
 #pragma unroll
                     for (int e = 0; e < V; ++e)
-                        t[threadIdx.x * V + e] = which ? dwi[l][0][e] : dwo[l][0][e];
+                        t[threadIdx.x * V + e] = which ? dwi[l][e] : dwo[l][e];
                     __syncthreads();
                     const int groups = workers * (32 / width);
                     for (int c = threadIdx.x; c < p.C; c += blockDim.x) {
@@ -442,14 +416,227 @@ __global__ void __launch_bounds__(256, (CTA && J * V <= 16 && L == 0) ? 2 : 1) b
     }
 }
 
+// ---------------------------------------------------------------------------
+// Wide rows (L = 0, more than 32 vectors across): a CTA takes a row out of its
+// slot into registers (8 channels a thread), frees the slot at its first
+// barrier, and does all arithmetic from registers, once per element.  What
+// bounds it, beside memory, is the instructions per element, so every factor
+// of a channel is formed once and the weights stay in registers.
+
+// The sum of v over the CTA; red: [2][16], zeros behind the last warp.
+struct CtaSum {
+    float* red;
+    int flip;
+    __device__ __forceinline__ float operator()(float v) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        float* r = red + flip * 16;
+        flip ^= 1;       // the next sum's buffer: one barrier a sum is enough
+        if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = v;
+        __syncthreads();
+        const float4* q = reinterpret_cast<const float4*>(r);
+        const float4 a = q[0], b = q[1], c = q[2], d = q[3];
+        return ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w)) + ((c.x + c.y) + (c.z + c.w)) +
+               ((d.x + d.y) + (d.z + d.w));
+    }
+};
+
+template <class T, int V, int J, bool BWD>
+__global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(const StagedParams s) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ uint64_t full[kMaxSlots];
+    __shared__ __align__(16) float red[2 * 16];
+    const BnParams& p = s.p;
+    const Ring ring{smem, full};
+    const bool post = p.b != nullptr, gated = p.gate != nullptr;
+    const bool pre = BWD ? p.g_h != nullptr : p.w_pre != nullptr, more = p.g_x != nullptr;
+    const int c0 = threadIdx.x * V, cstep = blockDim.x * V;
+    const float inv_m = 1.f / (float)p.C;
+    if (threadIdx.x < 32) red[threadIdx.x] = 0.f;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < s.slots; ++i) bulk::init(full + i);
+        bulk::fence_init();
+    }
+    __syncthreads();
+    if (threadIdx.x == 0)
+        for (int k = 0; k < s.slots; ++k) fill<BWD>(s, ring, k);
+    bool own[J];
+    float wo[J][V], wi[J][V], dwo[J][V], dwi[J][V];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        own[j] = c0 + j * cstep < p.C;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            wo[j][e] = own[j] && post ? __ldg(p.w_post + c0 + j * cstep + e) : 0.f;
+            wi[j][e] = own[j] && pre ? __ldg(p.w_pre + c0 + j * cstep + e) : 0.f;
+            dwo[j][e] = dwi[j][e] = 0.f;
+        }
+    }
+    CtaSum sum{red, 0};
+    const int mine = s.total > blockIdx.x ? (int)((s.total - blockIdx.x + gridDim.x - 1) / gridDim.x) : 0;
+    for (int k = 0, slot = 0, turn = 0; k < mine; ++k) {
+        const int64_t n = blockIdx.x + (int64_t)k * gridDim.x;
+        float sb = 0.f, sy = 0.f;
+        if constexpr (BWD) {
+            if (post) sb = __ldg(p.stats + n);
+            if (pre) sy = __ldg(p.stats + p.N + n);
+        }
+        if (!bulk::wait(full + slot, (uint32_t)turn & 1u)) {
+            // give up: the copies still in flight end first (each wait is bounded)
+            atomicOr(s.status, 4u);
+            if (threadIdx.x == 0)
+                for (int i = 0; i < s.slots; ++i) bulk::wait(full + i, 0), bulk::wait(full + i, 1);
+            return;
+        }
+        const unsigned char* base = ring.base + (int64_t)slot * s.slot_bytes;
+        const auto at = [&](int o, int j) { return reinterpret_cast<const T*>(base + o) + c0 + j * cstep; };
+        const auto release = [&] {       // behind a barrier: every thread has read the slot
+            if (threadIdx.x == 0) fill<BWD>(s, ring, k + s.slots);
+        };
+        // y: x, then x_out; bs: b, then b / rms(b); sa: scale a(gate)
+        float y[J][V], bs[J][V], sa[J][V], da[J][V];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            if (!own[j]) continue;
+            if (!BWD || pre) lds(y[j], at(s.o_x, j));
+            if (post) lds(bs[j], at(s.o_b, j));
+            if (gated) {
+                float g[V];
+                lds(g, at(s.o_g, j));
+                gate_values(p.gate_kind, g, sa[j], da[j]);
+#pragma unroll
+                for (int e = 0; e < V; ++e) sa[j][e] *= p.scale;
+            } else {
+#pragma unroll
+                for (int e = 0; e < V; ++e) sa[j][e] = p.scale;
+            }
+        }
+        if constexpr (!BWD) {
+            if (post) {
+                float v = 0.f;
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+                    if (own[j])
+#pragma unroll
+                        for (int e = 0; e < V; ++e) v = fmaf(bs[j][e], bs[j][e], v);
+                sb = rsqrtf(sum(v) * inv_m + p.eps);
+                release();
+            }
+            float v = 0.f;
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                if (own[j]) {
+                    if (post) {
+#pragma unroll
+                        for (int e = 0; e < V; ++e) y[j][e] = fmaf(sa[j][e] * wo[j][e], bs[j][e] * sb, y[j][e]);
+                        put(static_cast<T*>(p.x_out) + n * p.C + c0 + j * cstep, y[j]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < V; ++e) v = fmaf(y[j][e], y[j][e], v);
+                }
+            if (pre) {
+                sy = rsqrtf(sum(v) * inv_m + p.eps);
+                if (!post) release();
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+                    if (own[j]) {
+#pragma unroll
+                        for (int e = 0; e < V; ++e) y[j][e] = y[j][e] * sy * wi[j][e];
+                        put(static_cast<T*>(p.h) + n * p.C + c0 + j * cstep, y[j]);
+                    }
+            }
+            if (p.stats && threadIdx.x == 0) {
+                if (post) p.stats[n] = sb;
+                if (pre) p.stats[p.N + n] = sy;
+            }
+        } else {
+            float gx[J][V], gh[J][V];
+            float v = 0.f;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if (!own[j]) continue;
+                if (more) lds(gx[j], at(s.o_gx, j));
+                else
+#pragma unroll
+                    for (int e = 0; e < V; ++e) gx[j][e] = 0.f;
+                if (post)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) bs[j][e] *= sb;
+                if (pre) {
+                    lds(gh[j], at(s.o_gh, j));
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        if (post) y[j][e] = fmaf(sa[j][e] * wo[j][e], bs[j][e], y[j][e]);
+                        const float gy = gh[j][e] * y[j][e];
+                        v = fmaf(gy, wi[j][e], v);
+                        dwi[j][e] = fmaf(gy, sy, dwi[j][e]);
+                    }
+                }
+            }
+            float m1 = 0.f;
+            if (pre) {
+                m1 = sum(v) * inv_m * sy * sy * sy;
+                release();
+            }
+            v = 0.f;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if (!own[j]) continue;
+                // t, the gradient of x_out in all, in the place of gx
+                if (pre)
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        gx[j][e] = fmaf(-m1, y[j][e], fmaf(gh[j][e], sy * wi[j][e], gx[j][e]));
+                put(static_cast<T*>(p.dx) + n * p.C + c0 + j * cstep, gx[j]);
+                if (!post) continue;
+                float dg[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float tb = gx[j][e] * bs[j][e];
+                    dwo[j][e] = fmaf(sa[j][e], tb, dwo[j][e]);
+                    dg[e] = gated ? p.scale * da[j][e] * wo[j][e] * tb : 0.f;
+                    gx[j][e] *= sa[j][e] * wo[j][e];          // q
+                    v = fmaf(gx[j][e], bs[j][e], v);
+                }
+                if (gated) put(static_cast<T*>(p.dgate) + n * p.C + c0 + j * cstep, dg);
+            }
+            if (post) {
+                const float m2 = sum(v) * inv_m;
+                if (!pre) release();
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+                    if (own[j]) {
+#pragma unroll
+                        for (int e = 0; e < V; ++e) gx[j][e] = sb * fmaf(-bs[j][e], m2, gx[j][e]);
+                        put(static_cast<T*>(p.db) + n * p.C + c0 + j * cstep, gx[j]);
+                    }
+            }
+        }
+        if (++slot == s.slots) {
+            slot = 0;
+            ++turn;
+        }
+    }
+    if constexpr (BWD) {
+        float* part = p.part + (int64_t)blockIdx.x * 2 * p.C;
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            if (own[j]) {
+                put(part + c0 + j * cstep, dwo[j]);
+                put(part + p.C + c0 + j * cstep, dwi[j]);
+            }
+    }
+}
+
 // How a staged launch is cut; slots 0: not staged.
 struct Staged {
     int V, J, width, threads, slots, nodes, ctas, smem;
+    bool row;          // the kernel for wide rows
 };
 
 // Two slots at least, of what an SM's shared memory holds; workers that leave
 // two fifths of the slots to the copies in flight.
-inline Staged staged_shape(int L, int C, int es, int tensors, bool gated) {
+inline Staged staged_shape(int L, int C, int es, int tensors, bool gated, bool bwd) {
     Staged s{};
     const int room = 224 * 1024, wbytes = 2 * (L + 1) * C * 4;
     const int64_t node = (int64_t)(L + 1) * (L + 1) * C * es * tensors + (gated ? (int64_t)(L + 1) * C * es : 0);
@@ -470,14 +657,27 @@ inline Staged staged_shape(int L, int C, int es, int tensors, bool gated) {
         s.threads = 32 * warps;
         // the reduction of the weight gradients takes threads * V floats of the ring
         if ((int64_t)s.slots * s.nodes * node < (int64_t)s.threads * s.V * 4) return Staged{};
-    } else {
-        while (s.J < (L == 0 ? 4 : 1) && (vecs + s.J - 1) / s.J > 256) s.J *= 2;
-        const int across = (vecs + s.J - 1) / s.J;
-        if (across > 256) return Staged{};
-        s.width = s.threads = (across + 31) / 32 * 32;
+    } else if (L == 0) {
+        // 8 channels a thread, 16 for the widest 16-bit rows; 512 threads an SM (128 registers each) backward and
+        // for the widest, 1024 else
+        s.row = true;
+        s.J = s.V == 4 || vecs > 512 ? 2 : 1;
+        if (vecs > 512 * s.J) return Staged{};
+        s.width = s.threads = ((vecs + s.J - 1) / s.J + 31) / 32 * 32;
         s.nodes = 1;
-        s.ctas = L == 0 && s.J * s.V <= 16 && 2 * (wbytes + 2 * node) <= room ? 2 : 1;
-        const int64_t fit = (room / s.ctas - wbytes) / node;
+        s.ctas = (bwd || s.J * s.V > 8 ? 512 : 1024) / s.threads;
+        int64_t fit = (room / s.ctas - 1536) / node;      // barriers and what the system keeps of each CTA
+        while (fit < 2 && s.ctas > 1) fit = (room / --s.ctas - 1536) / node;
+        s.slots = (int)(fit < 4 ? fit : 4);
+        if (s.slots < 2) return Staged{};
+        s.smem = (int)node * s.slots;
+        return s;
+    } else {
+        if (vecs > 256) return Staged{};
+        s.width = s.threads = (vecs + 31) / 32 * 32;
+        s.nodes = 1;
+        s.ctas = 1;
+        const int64_t fit = (room - wbytes) / node;
         s.slots = (int)(fit < kMaxSlots ? fit : kMaxSlots);
         if (s.slots < 2) return Staged{};
     }
@@ -485,19 +685,35 @@ inline Staged staged_shape(int L, int C, int es, int tensors, bool gated) {
     return s;
 }
 
-template <class T, int V, int L, int J, bool BWD, bool CTA>
+template <class T, int V, int L, bool BWD, bool CTA>
 cudaError_t launch_staged(const StagedParams& s, const Staged& h, int grid, cudaStream_t st) {
     static bool done[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64 || !done[dev]) {
-        e = cudaFuncSetAttribute(bn_staged_kernel<T, V, L, J, BWD, CTA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(bn_staged_kernel<T, V, L, BWD, CTA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  225 * 1024);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) done[dev] = true;
     }
-    bn_staged_kernel<T, V, L, J, BWD, CTA><<<grid, h.threads, h.smem, st>>>(s);
+    bn_staged_kernel<T, V, L, BWD, CTA><<<grid, h.threads, h.smem, st>>>(s);
+    count_launch();
+    return cudaGetLastError();
+}
+
+template <class T, int V, int J, bool BWD>
+cudaError_t launch_row(const StagedParams& s, const Staged& h, int grid, cudaStream_t st) {
+    static bool done[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !done[dev]) {
+        e = cudaFuncSetAttribute(bn_row_kernel<T, V, J, BWD>, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) done[dev] = true;
+    }
+    bn_row_kernel<T, V, J, BWD><<<grid, h.threads, h.smem, st>>>(s);
     count_launch();
     return cudaGetLastError();
 }
@@ -506,21 +722,23 @@ template <class T, bool BWD>
 cudaError_t staged_for(const StagedParams& s, const Staged& h, int grid, cudaStream_t st) {
     constexpr int W = 16 / sizeof(T);
     const bool cta = h.width > 32;
+    if (h.row) {
+        if constexpr (W == 8)
+            if (h.J == 1) return launch_row<T, W, 1, BWD>(s, h, grid, st);
+        return launch_row<T, W, 2, BWD>(s, h, grid, st);
+    }
     switch (s.p.L) {
         case 0:
-            if (!cta) return launch_staged<T, W, 0, 1, BWD, false>(s, h, grid, st);
-            if (h.J == 1) return launch_staged<T, W, 0, 1, BWD, true>(s, h, grid, st);
-            if (h.J == 2) return launch_staged<T, W, 0, 2, BWD, true>(s, h, grid, st);
-            return launch_staged<T, W, 0, 4, BWD, true>(s, h, grid, st);
+            return launch_staged<T, W, 0, BWD, false>(s, h, grid, st);
         case 1:
-            return cta ? launch_staged<T, 4, 1, 1, BWD, true>(s, h, grid, st)
-                       : launch_staged<T, 4, 1, 1, BWD, false>(s, h, grid, st);
+            return cta ? launch_staged<T, 4, 1, BWD, true>(s, h, grid, st)
+                       : launch_staged<T, 4, 1, BWD, false>(s, h, grid, st);
         case 2:
-            return cta ? launch_staged<T, 4, 2, 1, BWD, true>(s, h, grid, st)
-                       : launch_staged<T, 4, 2, 1, BWD, false>(s, h, grid, st);
+            return cta ? launch_staged<T, 4, 2, BWD, true>(s, h, grid, st)
+                       : launch_staged<T, 4, 2, BWD, false>(s, h, grid, st);
         default:
-            return cta ? launch_staged<T, 4, 3, 1, BWD, true>(s, h, grid, st)
-                       : launch_staged<T, 4, 3, 1, BWD, false>(s, h, grid, st);
+            return cta ? launch_staged<T, 4, 3, BWD, true>(s, h, grid, st)
+                       : launch_staged<T, 4, 3, BWD, false>(s, h, grid, st);
     }
 }
 
