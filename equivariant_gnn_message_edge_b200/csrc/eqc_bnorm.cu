@@ -79,7 +79,8 @@ Shape shape_for(const BlockNormArgs& a) {
 Staged staged_for_args(const BlockNormArgs& a, bool bwd) {
     uintptr_t all = 0;
     for (const void* q : {a.x, a.b, a.gate, (const void*)a.x_out, (const void*)a.h, a.g_x, a.g_h,
-                          (const void*)a.dx, (const void*)a.db, (const void*)a.dgate})
+                          (const void*)a.dx, (const void*)a.db, (const void*)a.dgate, (const void*)a.w_post,
+                          (const void*)a.w_pre})
         all |= reinterpret_cast<uintptr_t>(q);
     if (all % 16 != 0) return Staged{};
     const int tensors = bwd ? 2 * (a.g_h != nullptr) + (a.b != nullptr) + (a.g_x != nullptr) : 1 + (a.b != nullptr);

@@ -48,43 +48,87 @@ struct BnParams {
     int width;           // threads across the channels of a group (a power of two up to 32, or whole warps)
 };
 
-// a(g) and a'(g) of V gates, of one kind (EQCONV_GATE_*).  exp and 1/x are the
-// hardware's approximations: a few units in the last place of fp32, and |g|
-// more of them through exp's argument.  tanh is (1 - q) / (1 + q) of
-// q = exp(-2 |g|), and near 0, where that cancels, its Taylor series (for
-// |g| < 0.25 the first term left out is below 2^-28 of the value).
+// 2^x and 1/x by the hardware's approximations (2 and 1 units in the last
+// place of fp32); results below the normal range become 0.
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// a(g) and a'(g) of V gates (pairs), of one kind (EQCONV_GATE_*).  The error is
+// a few units in the last place of fp32, and |g| more of them through the
+// rounded argument of the power.  tanh is (1 - q) / (1 + q) of q = exp(-2 |g|),
+// and near 0, where that cancels, its Taylor series (for |g| < 0.25 the first
+// term left out is below 2^-28 of the value).
 template <int V>
-__device__ __forceinline__ void gate_values(int kind, const float (&g)[V], float (&a)[V], float (&da)[V]) {
+__device__ __forceinline__ void gate_values(int kind, const F2 (&g)[V / 2], F2 (&a)[V / 2], F2 (&da)[V / 2]) {
+    constexpr float kLog2e = 1.4426950408889634f;
+    const F2 one(1.f), minus(-1.f);
     if (kind == 3) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const float q = __expf(-2.f * fabsf(g[e])), g2 = g[e] * g[e];
-            const float far = copysignf(__fdividef(1.f - q, 1.f + q), g[e]);
-            float c = fmaf(g2, -1382.f / 155925.f, 62.f / 2835.f);
-            c = fmaf(g2, c, -17.f / 315.f);
-            c = fmaf(g2, c, 2.f / 15.f);
-            c = fmaf(g2, c, -1.f / 3.f);
-            const float near = fmaf(g[e] * g2, c, g[e]);
-            a[e] = g2 < 0.0625f ? near : far;
-            da[e] = fmaf(-a[e], a[e], 1.f);
+        for (int i = 0; i < V / 2; ++i) {
+            float x, y;
+            g[i].split(x, y);
+            const float qx = exp2_fast(-2.f * kLog2e * fabsf(x)), qy = exp2_fast(-2.f * kLog2e * fabsf(y));
+            const F2 q(qx, qy), g2 = mul2(g[i], g[i]);
+            float nx, ny, dx, dy, sx, sy, fx, fy;
+            fma2(q, minus, one).split(nx, ny);
+            add2(q, one).split(dx, dy);
+            F2 c = fma2(g2, F2(-1382.f / 155925.f), F2(62.f / 2835.f));
+            c = fma2(g2, c, F2(-17.f / 315.f));
+            c = fma2(g2, c, F2(2.f / 15.f));
+            c = fma2(g2, c, F2(-1.f / 3.f));
+            fma2(mul2(g[i], g2), c, g[i]).split(sx, sy);
+            fx = copysignf(nx * rcp_fast(dx), x);
+            fy = copysignf(ny * rcp_fast(dy), y);
+            a[i] = F2(fabsf(x) < 0.25f ? sx : fx, fabsf(y) < 0.25f ? sy : fy);
+            da[i] = fma2(mul2(a[i], minus), a[i], one);
         }
     } else {
-        float s[V];
+        F2 s[V / 2], r[V / 2];      // the sigmoid, and 1 minus it
 #pragma unroll
-        for (int e = 0; e < V; ++e) s[e] = __fdividef(1.f, 1.f + __expf(-g[e]));
+        for (int i = 0; i < V / 2; ++i) {
+            float x, y;
+            g[i].split(x, y);
+            s[i] = F2(rcp_fast(1.f + exp2_fast(-kLog2e * x)), rcp_fast(1.f + exp2_fast(-kLog2e * y)));
+            r[i] = fma2(s[i], minus, one);
+        }
         if (kind == 1) {
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                a[e] = s[e];
-                da[e] = s[e] * (1.f - s[e]);
+            for (int i = 0; i < V / 2; ++i) {
+                a[i] = s[i];
+                da[i] = mul2(s[i], r[i]);
             }
         } else {
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                a[e] = g[e] * s[e];
-                da[e] = s[e] * fmaf(g[e], 1.f - s[e], 1.f);
+            for (int i = 0; i < V / 2; ++i) {
+                a[i] = mul2(g[i], s[i]);
+                da[i] = mul2(s[i], fma2(g[i], r[i], one));
             }
         }
+    }
+}
+
+template <int V>
+__device__ __forceinline__ void gate_values(int kind, const float (&g)[V], float (&a)[V], float (&da)[V]) {
+    constexpr int W = (V + 1) / 2 * 2;
+    F2 gv[W / 2], av[W / 2], dv[W / 2];
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) gv[i] = F2(g[2 * i], 2 * i + 1 < V ? g[2 * i + 1] : 0.f);
+    gate_values<W>(kind, gv, av, dv);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        float x, y;
+        av[e / 2].split(x, y);
+        a[e] = e & 1 ? y : x;
+        dv[e / 2].split(x, y);
+        da[e] = e & 1 ? y : x;
     }
 }
 

@@ -59,31 +59,10 @@ struct View {
     const T *x, *b, *gx, *gh, *g;
 };
 
-template <class T, int V>
-__device__ __forceinline__ void lds(float (&v)[V], const T* p) {
-    Pack<T, V> k;
-    if constexpr (Pack<T, V>::kPiece == 16) {
-#pragma unroll
-        for (int i = 0; i < Pack<T, V>::kBytes / 16; ++i) k.q[i] = reinterpret_cast<const uint4*>(p)[i];
-    } else {
-        static_assert(Pack<T, V>::kPiece == 8, "four 16-bit channels");
-        k.d = *reinterpret_cast<const uint2*>(p);
-    }
-#pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = k.get(e);
-}
-
-template <class T, int V>
-__device__ __forceinline__ void put(T* p, const float (&v)[V]) {
-    Pack<T, V> o;
-#pragma unroll
-    for (int e = 0; e < V; ++e) o.set(e, v[e]);
-    o.store(p);
-}
-
 template <class T, int V, int L>
 __device__ __forceinline__ void fwd_node(const BnParams& p, const View<T>& s, const float* w, bool own, bool live,
                                          int64_t row, int64_t srow, int c0, bool lead, WorkerSum<L + 1>& sum) {
+    constexpr int H = V / 2;
     const bool post = p.b != nullptr, pre = p.w_pre != nullptr, gated = p.gate != nullptr;
     float sb[L + 1], sy[L + 1];
 #pragma unroll
@@ -91,71 +70,76 @@ __device__ __forceinline__ void fwd_node(const BnParams& p, const View<T>& s, co
     if (post) {
 #pragma unroll
         for (int l = 0; l <= L; ++l)
-            if (own)
+            if (own) {
+                F2 v(0.f);
 #pragma unroll
                 for (int m = 0; m < 2 * l + 1; ++m) {
-                    float b[V];
-                    lds(b, s.b + (l * l + m) * p.C);
+                    F2 b[H];
+                    load2<T, V>(b, s.b + (l * l + m) * p.C);
 #pragma unroll
-                    for (int e = 0; e < V; ++e) sb[l] += b[e] * b[e];
+                    for (int i = 0; i < H; ++i) v = fma2(b[i], b[i], v);
                 }
+                sb[l] = v.sum();
+            }
         sum(sb);
     }
-    float k[L + 1][V];
+    F2 k[L + 1][H];                  // y = x + k b
 #pragma unroll
     for (int l = 0; l <= L; ++l) {
         if (post) sb[l] = rsqrtf(sb[l] * (1.f / ((2 * l + 1) * (float)p.C)) + p.eps);
-        if (own) {
-            if (post) {
-                float wo[V];
-                lds(wo, w + l * p.C + c0);
+        if (!own) continue;
+        if (post) {
+            load2<float, V>(k[l], w + l * p.C + c0);
 #pragma unroll
-                for (int e = 0; e < V; ++e) k[l][e] = p.scale * sb[l] * wo[e];
-                if (gated) {
-                    float g[V];
-                    lds(g, s.g + l * p.C);
-                    float a[V], da[V];
-                    gate_values(p.gate_kind, g, a, da);
+            for (int i = 0; i < H; ++i) k[l][i] = mul2(k[l][i], F2(p.scale * sb[l]));
+            if (gated) {
+                F2 g[H], a[H], da[H];
+                load2<T, V>(g, s.g + l * p.C);
+                gate_values<V>(p.gate_kind, g, a, da);
 #pragma unroll
-                    for (int e = 0; e < V; ++e) k[l][e] *= a[e];
-                }
-            }
-#pragma unroll
-            for (int m = 0; m < 2 * l + 1; ++m) {
-                float y[V], b[V];
-                lds(y, s.x + (l * l + m) * p.C);
-                if (post) {
-                    lds(b, s.b + (l * l + m) * p.C);
-#pragma unroll
-                    for (int e = 0; e < V; ++e) y[e] += k[l][e] * b[e];
-                    if (live) put(static_cast<T*>(p.x_out) + row + (l * l + m) * p.C + c0, y);
-                }
-#pragma unroll
-                for (int e = 0; e < V; ++e) sy[l] += y[e] * y[e];
+                for (int i = 0; i < H; ++i) k[l][i] = mul2(k[l][i], a[i]);
             }
         }
+        F2 v(0.f);
+#pragma unroll
+        for (int m = 0; m < 2 * l + 1; ++m) {
+            F2 y[H];
+            load2<T, V>(y, s.x + (l * l + m) * p.C);
+            if (post) {
+                F2 b[H];
+                load2<T, V>(b, s.b + (l * l + m) * p.C);
+#pragma unroll
+                for (int i = 0; i < H; ++i) y[i] = fma2(k[l][i], b[i], y[i]);
+                if (live) store2<T, V>(static_cast<T*>(p.x_out) + row + (l * l + m) * p.C + c0, y);
+            }
+#pragma unroll
+            for (int i = 0; i < H; ++i) v = fma2(y[i], y[i], v);
+        }
+        sy[l] = v.sum();
     }
     if (pre) {
         sum(sy);
 #pragma unroll
         for (int l = 0; l <= L; ++l) {
             sy[l] = rsqrtf(sy[l] * (1.f / ((2 * l + 1) * (float)p.C)) + p.eps);
-            if (own) {
-                float wi[V];
-                lds(wi, w + (L + 1 + l) * p.C + c0);
+            if (!own) continue;
+            F2 wi[H];
+            load2<float, V>(wi, w + (L + 1 + l) * p.C + c0);
 #pragma unroll
-                for (int m = 0; m < 2 * l + 1; ++m) {
-                    float y[V], b[V];
-                    lds(y, s.x + (l * l + m) * p.C);
-                    if (post) {
-                        lds(b, s.b + (l * l + m) * p.C);
+            for (int i = 0; i < H; ++i) wi[i] = mul2(wi[i], F2(sy[l]));
 #pragma unroll
-                        for (int e = 0; e < V; ++e) y[e] += k[l][e] * b[e];
-                    }
+            for (int m = 0; m < 2 * l + 1; ++m) {
+                F2 y[H];
+                load2<T, V>(y, s.x + (l * l + m) * p.C);
+                if (post) {
+                    F2 b[H];
+                    load2<T, V>(b, s.b + (l * l + m) * p.C);
 #pragma unroll
-                    for (int e = 0; e < V; ++e) y[e] *= sy[l] * wi[e];
-                    if (live) put(static_cast<T*>(p.h) + row + (l * l + m) * p.C + c0, y);
+                    for (int i = 0; i < H; ++i) y[i] = fma2(k[l][i], b[i], y[i]);
                 }
+#pragma unroll
+                for (int i = 0; i < H; ++i) y[i] = mul2(y[i], wi[i]);
+                if (live) store2<T, V>(static_cast<T*>(p.h) + row + (l * l + m) * p.C + c0, y);
             }
         }
     }
@@ -167,144 +151,155 @@ __device__ __forceinline__ void fwd_node(const BnParams& p, const View<T>& s, co
         }
 }
 
+// kKeep (fp32): t goes into the slot in the place of g_h, so that db needs no
+// second pass over x, g_x and g_h; 16 bits would round it, so it is made again.
 template <class T, int V, int L>
 __device__ __forceinline__ void bwd_node(const BnParams& p, const View<T>& s, const float* w, bool own, bool live,
                                          int64_t row, int64_t grow, int c0, const float (&sb)[L + 1],
-                                         const float (&sy)[L + 1], float (&dwo)[L + 1][V], float (&dwi)[L + 1][V],
+                                         const float (&sy)[L + 1], F2 (&dwo)[L + 1][V / 2], F2 (&dwi)[L + 1][V / 2],
                                          WorkerSum<L + 1>& sum) {
+    constexpr int H = V / 2;
+    constexpr bool kKeep = sizeof(T) == 4;
     const bool post = p.b != nullptr, pre = p.g_h != nullptr, gated = p.gate != nullptr, more = p.g_x != nullptr;
-    float sa[L + 1][V], da[L + 1][V];     // scale a(gate), scale a'(gate)
+    F2 sa[L + 1][H], da[L + 1][H];     // scale a(gate), scale a'(gate)
     float mpy[L + 1], mqb[L + 1];
     // y of a row: x + k b with k = sa sb w_post
-    const auto y_of = [&](int r, const float (&k)[V], const float (&b)[V], float (&y)[V]) {
-        lds(y, s.x + r * p.C);
+    const auto y_of = [&](int r, const F2 (&k)[H], const F2 (&b)[H], F2 (&y)[H]) {
+        load2<T, V>(y, s.x + r * p.C);
         if (post)
 #pragma unroll
-            for (int e = 0; e < V; ++e) y[e] += k[e] * b[e];
+            for (int i = 0; i < H; ++i) y[i] = fma2(k[i], b[i], y[i]);
     };
 #pragma unroll
     for (int l = 0; l <= L; ++l) {
         mpy[l] = mqb[l] = 0.f;
-        if (own) {
-            if (gated) {
-                float g[V];
-                lds(g, s.g + l * p.C);
-                gate_values(p.gate_kind, g, sa[l], da[l]);
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    sa[l][e] *= p.scale;
-                    da[l][e] *= p.scale;
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    sa[l][e] = p.scale;
-                    da[l][e] = 0.f;
-                }
-            }
-            if (!pre) continue;
-            float wi[V], k[V], b[V];
-            lds(wi, w + (L + 1 + l) * p.C + c0);
-            if (post) {
-                lds(k, w + l * p.C + c0);
-#pragma unroll
-                for (int e = 0; e < V; ++e) k[e] *= sa[l][e] * sb[l];
-            }
-#pragma unroll
-            for (int m = 0; m < 2 * l + 1; ++m) {
-                float gh[V], y[V];
-                if (post) lds(b, s.b + (l * l + m) * p.C);
-                y_of(l * l + m, k, b, y);
-                lds(gh, s.gh + (l * l + m) * p.C);
-#pragma unroll
-                for (int e = 0; e < V; ++e) mpy[l] += gh[e] * wi[e] * y[e];
-            }
+        if (!own) continue;
+        if (gated) {
+            F2 g[H];
+            load2<T, V>(g, s.g + l * p.C);
+            gate_values<V>(p.gate_kind, g, sa[l], da[l]);
         }
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            sa[l][i] = gated ? mul2(sa[l][i], F2(p.scale)) : F2(p.scale);
+            da[l][i] = gated ? mul2(da[l][i], F2(p.scale)) : F2(0.f);
+        }
+        if (!pre) continue;
+        F2 wi[H], k[H], b[H], v(0.f);
+        load2<float, V>(wi, w + (L + 1 + l) * p.C + c0);
+        if (post) {
+            load2<float, V>(k, w + l * p.C + c0);
+#pragma unroll
+            for (int i = 0; i < H; ++i) k[i] = mul2(mul2(k[i], sa[l][i]), F2(sb[l]));
+        }
+#pragma unroll
+        for (int m = 0; m < 2 * l + 1; ++m) {
+            F2 gh[H], y[H];
+            if (post) load2<T, V>(b, s.b + (l * l + m) * p.C);
+            y_of(l * l + m, k, b, y);
+            load2<T, V>(gh, s.gh + (l * l + m) * p.C);
+#pragma unroll
+            for (int i = 0; i < H; ++i) v = fma2(mul2(gh[i], wi[i]), y[i], v);
+        }
+        mpy[l] = v.sum();
     }
     if (pre) {
         sum(mpy);
 #pragma unroll
-        for (int l = 0; l <= L; ++l) mpy[l] *= sy[l] * sy[l] * (1.f / ((2 * l + 1) * (float)p.C));
+        for (int l = 0; l <= L; ++l) mpy[l] *= sy[l] * sy[l] * sy[l] * (1.f / ((2 * l + 1) * (float)p.C));
     }
 #pragma unroll
-    for (int l = 0; l <= L; ++l)
-        if (own) {
-            float wi[V], wo[V], k[V], tb[V], gy[V];
-            if (pre) lds(wi, w + (L + 1 + l) * p.C + c0);
-            if (post) lds(wo, w + l * p.C + c0);
+    for (int l = 0; l <= L; ++l) {
+        if (!own) continue;
+        F2 wi[H], wo[H], k[H], tb[H], gy[H];      // wi: sy w_pre
+        if (pre) load2<float, V>(wi, w + (L + 1 + l) * p.C + c0);
+        if (post) load2<float, V>(wo, w + l * p.C + c0);
+        const F2 m1(-mpy[l]), s1(sy[l]), s0(sb[l]);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                tb[e] = gy[e] = 0.f;
-                k[e] = post ? wo[e] * sa[l][e] * sb[l] : 0.f;
-            }
-#pragma unroll
-            for (int m = 0; m < 2 * l + 1; ++m) {
-                const int r = l * l + m;
-                float t[V], b[V];
-                if (post) lds(b, s.b + r * p.C);
-                if (more) lds(t, s.gx + r * p.C);
-                else
-#pragma unroll
-                    for (int e = 0; e < V; ++e) t[e] = 0.f;
-                if (pre) {
-                    float gh[V], y[V];
-                    y_of(r, k, b, y);
-                    lds(gh, s.gh + r * p.C);
-#pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        t[e] += sy[l] * (gh[e] * wi[e] - y[e] * mpy[l]);
-                        gy[e] += gh[e] * y[e];
-                    }
-                }
-                if (post)
-#pragma unroll
-                    for (int e = 0; e < V; ++e) tb[e] += t[e] * b[e];
-                if (live) put(static_cast<T*>(p.dx) + row + r * p.C + c0, t);
-            }
-            float dg[V];
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                if (post) {
-                    const float u = sa[l][e] * tb[e];
-                    mqb[l] += u * wo[e];
-                    if (live) dwo[l][e] += u * sb[l];
-                    dg[e] = da[l][e] * sb[l] * wo[e] * tb[e];
-                }
-                if (live && pre) dwi[l][e] += sy[l] * gy[e];
-            }
-            if (gated && live) put(static_cast<T*>(p.dgate) + grow + l * p.C + c0, dg);
+        for (int i = 0; i < H; ++i) {
+            tb[i] = gy[i] = F2(0.f);
+            if (pre) wi[i] = mul2(wi[i], s1);
+            if (post) k[i] = mul2(mul2(wo[i], sa[l][i]), s0);
         }
+#pragma unroll
+        for (int m = 0; m < 2 * l + 1; ++m) {
+            const int r = l * l + m;
+            F2 t[H], b[H];
+            if (post) load2<T, V>(b, s.b + r * p.C);
+            if (more) load2<T, V>(t, s.gx + r * p.C);
+            else
+#pragma unroll
+                for (int i = 0; i < H; ++i) t[i] = F2(0.f);
+            if (pre) {
+                F2 gh[H], y[H];
+                y_of(r, k, b, y);
+                load2<T, V>(gh, s.gh + r * p.C);
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    t[i] = fma2(gh[i], wi[i], fma2(y[i], m1, t[i]));
+                    gy[i] = fma2(gh[i], y[i], gy[i]);
+                }
+                if constexpr (kKeep)
+                    if (post) store2<T, V>(const_cast<T*>(s.gh) + r * p.C, t);
+            }
+            if (post)
+#pragma unroll
+                for (int i = 0; i < H; ++i) tb[i] = fma2(t[i], b[i], tb[i]);
+            if (live) store2<T, V>(static_cast<T*>(p.dx) + row + r * p.C + c0, t);
+        }
+        F2 v(0.f), dg[H];
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            if (post) {
+                const F2 u = mul2(tb[i], s0);
+                v = fma2(mul2(sa[l][i], wo[i]), tb[i], v);
+                if (live) dwo[l][i] = fma2(sa[l][i], u, dwo[l][i]);
+                dg[i] = mul2(mul2(da[l][i], wo[i]), u);
+            }
+            if (live && pre) dwi[l][i] = fma2(gy[i], s1, dwi[l][i]);
+        }
+        mqb[l] = v.sum();
+        if (gated && live) store2<T, V>(static_cast<T*>(p.dgate) + grow + l * p.C + c0, dg);
+    }
     if (!post) return;
     sum(mqb);
 #pragma unroll
     for (int l = 0; l <= L; ++l) {
-        mqb[l] *= sb[l] * sb[l] * (1.f / ((2 * l + 1) * (float)p.C));
-        if (own) {
-            float wi[V], wo[V], k[V];
-            if (pre) lds(wi, w + (L + 1 + l) * p.C + c0);
-            lds(wo, w + l * p.C + c0);
+        mqb[l] *= sb[l] * sb[l] * sb[l] * (1.f / ((2 * l + 1) * (float)p.C));
+        if (!own) continue;
+        F2 wi[H], k[H];
+        const F2 m1(-mpy[l]), m2(-mqb[l]);
+        load2<float, V>(k, w + l * p.C + c0);
 #pragma unroll
-            for (int e = 0; e < V; ++e) k[e] = wo[e] * sa[l][e] * sb[l];
+        for (int i = 0; i < H; ++i) k[i] = mul2(mul2(k[i], sa[l][i]), F2(sb[l]));
+        if (pre && !kKeep) {
+            load2<float, V>(wi, w + (L + 1 + l) * p.C + c0);
 #pragma unroll
-            for (int m = 0; m < 2 * l + 1; ++m) {
-                const int r = l * l + m;
-                float t[V], b[V];
-                lds(b, s.b + r * p.C);
-                if (more) lds(t, s.gx + r * p.C);
+            for (int i = 0; i < H; ++i) wi[i] = mul2(wi[i], F2(sy[l]));
+        }
+#pragma unroll
+        for (int m = 0; m < 2 * l + 1; ++m) {
+            const int r = l * l + m;
+            F2 t[H], b[H];
+            load2<T, V>(b, s.b + r * p.C);
+            if (pre && kKeep) {
+                load2<T, V>(t, s.gh + r * p.C);
+            } else {
+                if (more) load2<T, V>(t, s.gx + r * p.C);
                 else
 #pragma unroll
-                    for (int e = 0; e < V; ++e) t[e] = 0.f;
+                    for (int i = 0; i < H; ++i) t[i] = F2(0.f);
                 if (pre) {
-                    float gh[V], y[V];
+                    F2 gh[H], y[H];
                     y_of(r, k, b, y);
-                    lds(gh, s.gh + r * p.C);
+                    load2<T, V>(gh, s.gh + r * p.C);
 #pragma unroll
-                    for (int e = 0; e < V; ++e) t[e] += sy[l] * (gh[e] * wi[e] - y[e] * mpy[l]);
+                    for (int i = 0; i < H; ++i) t[i] = fma2(gh[i], wi[i], fma2(y[i], m1, t[i]));
                 }
-#pragma unroll
-                for (int e = 0; e < V; ++e) t[e] = k[e] * t[e] - sb[l] * b[e] * mqb[l];
-                if (live) put(static_cast<T*>(p.db) + row + r * p.C + c0, t);
             }
+#pragma unroll
+            for (int i = 0; i < H; ++i) t[i] = fma2(k[i], t[i], mul2(b[i], m2));
+            if (live) store2<T, V>(static_cast<T*>(p.db) + row + r * p.C + c0, t);
         }
     }
 }
@@ -336,14 +331,26 @@ __global__ void __launch_bounds__(256, 1) bn_staged_kernel(const StagedParams s)
     if (threadIdx.x == 0)
         for (int k = 0; k < s.slots; ++k) fill<BWD>(s, ring, k);
     const bool own = c0 < p.C;
-    float dwo[BWD ? L + 1 : 1][V], dwi[BWD ? L + 1 : 1][V];
+    F2 dwo[BWD ? L + 1 : 1][V / 2], dwi[BWD ? L + 1 : 1][V / 2];
 #pragma unroll
     for (int l = 0; l < (BWD ? L + 1 : 1); ++l)
 #pragma unroll
-        for (int e = 0; e < V; ++e) dwo[l][e] = dwi[l][e] = 0.f;
+        for (int i = 0; i < V / 2; ++i) dwo[l][i] = dwi[l][i] = F2(0.f);
     WorkerSum<L + 1> sum{red, width, 0};
     const int mine = s.total > blockIdx.x ? (int)((s.total - blockIdx.x + gridDim.x - 1) / gridDim.x) : 0;
     bool ok = true;
+    // a node's statistics are fetched while the worker's last node is worked on
+    float sb_next[BWD ? L + 1 : 1], sy_next[BWD ? L + 1 : 1];
+    const auto fetch = [&](int k) {
+        const int64_t n = (blockIdx.x + (int64_t)k * gridDim.x) * s.nodes + sub;
+#pragma unroll
+        for (int l = 0; l < (BWD ? L + 1 : 1); ++l) {
+            sb_next[l] = n < p.N && p.b ? __ldg(p.stats + n * (L + 1) + l) : 0.f;
+            sy_next[l] = n < p.N && p.g_h ? __ldg(p.stats + ((int64_t)p.N + n) * (L + 1) + l) : 0.f;
+        }
+    };
+    if constexpr (BWD)
+        if (worker < mine) fetch(worker);
     for (int k = worker; k < mine; k += workers) {
         const int slot = k % s.slots;
         const int64_t n = (blockIdx.x + (int64_t)k * gridDim.x) * s.nodes + sub;
@@ -351,10 +358,8 @@ __global__ void __launch_bounds__(256, 1) bn_staged_kernel(const StagedParams s)
         float sb[L + 1], sy[L + 1];
         if constexpr (BWD) {
 #pragma unroll
-            for (int l = 0; l <= L; ++l) {
-                sb[l] = live && p.b ? __ldg(p.stats + n * (L + 1) + l) : 0.f;
-                sy[l] = live && p.g_h ? __ldg(p.stats + ((int64_t)p.N + n) * (L + 1) + l) : 0.f;
-            }
+            for (int l = 0; l <= L; ++l) sb[l] = sb_next[l], sy[l] = sy_next[l];
+            fetch(k + workers);
         }
         if (!bulk::wait(full + slot, (uint32_t)(k / s.slots) & 1u)) {
             atomicOr(s.status, 4u);
@@ -372,7 +377,8 @@ __global__ void __launch_bounds__(256, 1) bn_staged_kernel(const StagedParams s)
             bwd_node<T, V, L>(p, v, w, own, live, row, grow, c0, sb, sy, dwo, dwi, sum);
         else
             fwd_node<T, V, L>(p, v, w, own, live, row, n * (L + 1), c0, x0 == 0, sum);
-        // everyone has read the slot: its next copies may come
+        // everyone has read (and written) the slot: its next copies may come
+        if constexpr (BWD && sizeof(T) == 4) bulk::fence_writes();
         if constexpr (CTA) __syncthreads();
         else __syncwarp();
         if (lane == 0) fill<BWD>(s, ring, k + s.slots);
@@ -389,8 +395,8 @@ __global__ void __launch_bounds__(256, 1) bn_staged_kernel(const StagedParams s)
 #pragma unroll
             for (int l = 0; l <= L; ++l)
                 if (own) {
-                    put(part + l * p.C + c0, dwo[l]);
-                    put(part + (L + 1 + l) * p.C + c0, dwi[l]);
+                    store2<float, V>(part + l * p.C + c0, dwo[l]);
+                    store2<float, V>(part + (L + 1 + l) * p.C + c0, dwi[l]);
                 }
         } else {
             // the warps' sums in order, and within a warp its nodes', one degree and kind at a time
@@ -400,9 +406,7 @@ __global__ void __launch_bounds__(256, 1) bn_staged_kernel(const StagedParams s)
             for (int l = 0; l <= L; ++l)
 #pragma unroll
                 for (int which = 0; which < 2; ++which) {
-#pragma unroll
-                    for (int e = 0; e < V; ++e)
-                        t[threadIdx.x * V + e] = which ? dwi[l][e] : dwo[l][e];
+                    store2<float, V>(t + threadIdx.x * V, which ? dwi[l] : dwo[l]);
                     __syncthreads();
                     const int groups = workers * (32 / width);
                     for (int c = threadIdx.x; c < p.C; c += blockDim.x) {
@@ -460,27 +464,31 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
     __syncthreads();
     if (threadIdx.x == 0)
         for (int k = 0; k < s.slots; ++k) fill<BWD>(s, ring, k);
+    constexpr int H = V / 2;
     bool own[J];
-    float wo[J][V], wi[J][V], dwo[J][V], dwi[J][V];
+    F2 wo[J][H], wi[J][H], dwo[J][H], dwi[J][H];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
         own[j] = c0 + j * cstep < p.C;
+        if (own[j] && post) load2<float, V>(wo[j], p.w_post + c0 + j * cstep);
+        if (own[j] && pre) load2<float, V>(wi[j], p.w_pre + c0 + j * cstep);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            wo[j][e] = own[j] && post ? __ldg(p.w_post + c0 + j * cstep + e) : 0.f;
-            wi[j][e] = own[j] && pre ? __ldg(p.w_pre + c0 + j * cstep + e) : 0.f;
-            dwo[j][e] = dwi[j][e] = 0.f;
-        }
+        for (int i = 0; i < H; ++i) dwo[j][i] = dwi[j][i] = F2(0.f);
     }
     CtaSum sum{red, 0};
+    const F2 scale(p.scale);
     const int mine = s.total > blockIdx.x ? (int)((s.total - blockIdx.x + gridDim.x - 1) / gridDim.x) : 0;
+    // a row's statistics are fetched while the row before is worked on
+    float sb_next = 0.f, sy_next = 0.f;
+    const auto fetch = [&](int64_t n) {
+        if (post && n < p.N) sb_next = __ldg(p.stats + n);
+        if (pre && n < p.N) sy_next = __ldg(p.stats + p.N + n);
+    };
+    if constexpr (BWD) fetch(blockIdx.x);
     for (int k = 0, slot = 0, turn = 0; k < mine; ++k) {
         const int64_t n = blockIdx.x + (int64_t)k * gridDim.x;
-        float sb = 0.f, sy = 0.f;
-        if constexpr (BWD) {
-            if (post) sb = __ldg(p.stats + n);
-            if (pre) sy = __ldg(p.stats + p.N + n);
-        }
+        float sb = sb_next, sy = sy_next;
+        if constexpr (BWD) fetch(n + gridDim.x);
         if (!bulk::wait(full + slot, (uint32_t)turn & 1u)) {
             // give up: the copies still in flight end first (each wait is bounded)
             atomicOr(s.status, 4u);
@@ -490,59 +498,65 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
         }
         const unsigned char* base = ring.base + (int64_t)slot * s.slot_bytes;
         const auto at = [&](int o, int j) { return reinterpret_cast<const T*>(base + o) + c0 + j * cstep; };
+        const auto to = [&](void* q, int j) { return static_cast<T*>(q) + n * p.C + c0 + j * cstep; };
         const auto release = [&] {       // behind a barrier: every thread has read the slot
             if (threadIdx.x == 0) fill<BWD>(s, ring, k + s.slots);
         };
-        // y: x, then x_out; bs: b, then b / rms(b); sa: scale a(gate)
-        float y[J][V], bs[J][V], sa[J][V], da[J][V];
+        // y: x, then x_out; bs: b, then b / rms(b); sa, da: scale a(gate), scale a'(gate)
+        F2 y[J][H], bs[J][H], sa[J][H], da[J][H];
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             if (!own[j]) continue;
-            if (!BWD || pre) lds(y[j], at(s.o_x, j));
-            if (post) lds(bs[j], at(s.o_b, j));
+            if (!BWD || pre) load2<T, V>(y[j], at(s.o_x, j));
+            if (post) load2<T, V>(bs[j], at(s.o_b, j));
             if (gated) {
-                float g[V];
-                lds(g, at(s.o_g, j));
-                gate_values(p.gate_kind, g, sa[j], da[j]);
+                F2 g[H];
+                load2<T, V>(g, at(s.o_g, j));
+                gate_values<V>(p.gate_kind, g, sa[j], da[j]);
 #pragma unroll
-                for (int e = 0; e < V; ++e) sa[j][e] *= p.scale;
+                for (int i = 0; i < H; ++i) sa[j][i] = mul2(sa[j][i], scale);
             } else {
 #pragma unroll
-                for (int e = 0; e < V; ++e) sa[j][e] = p.scale;
+                for (int i = 0; i < H; ++i) sa[j][i] = scale;
             }
         }
         if constexpr (!BWD) {
             if (post) {
-                float v = 0.f;
+                F2 v(0.f);
 #pragma unroll
                 for (int j = 0; j < J; ++j)
                     if (own[j])
 #pragma unroll
-                        for (int e = 0; e < V; ++e) v = fmaf(bs[j][e], bs[j][e], v);
-                sb = rsqrtf(sum(v) * inv_m + p.eps);
+                        for (int i = 0; i < H; ++i) {
+                            v = fma2(bs[j][i], bs[j][i], v);
+                            sa[j][i] = mul2(sa[j][i], wo[j][i]);
+                        }
+                sb = rsqrtf(sum(v.sum()) * inv_m + p.eps);
                 release();
             }
-            float v = 0.f;
+            F2 v(0.f);
+            const F2 s0(sb);
 #pragma unroll
             for (int j = 0; j < J; ++j)
                 if (own[j]) {
                     if (post) {
 #pragma unroll
-                        for (int e = 0; e < V; ++e) y[j][e] = fmaf(sa[j][e] * wo[j][e], bs[j][e] * sb, y[j][e]);
-                        put(static_cast<T*>(p.x_out) + n * p.C + c0 + j * cstep, y[j]);
+                        for (int i = 0; i < H; ++i) y[j][i] = fma2(sa[j][i], mul2(bs[j][i], s0), y[j][i]);
+                        store2<T, V>(to(p.x_out, j), y[j]);
                     }
 #pragma unroll
-                    for (int e = 0; e < V; ++e) v = fmaf(y[j][e], y[j][e], v);
+                    for (int i = 0; i < H; ++i) v = fma2(y[j][i], y[j][i], v);
                 }
             if (pre) {
-                sy = rsqrtf(sum(v) * inv_m + p.eps);
+                sy = rsqrtf(sum(v.sum()) * inv_m + p.eps);
                 if (!post) release();
+                const F2 s1(sy);
 #pragma unroll
                 for (int j = 0; j < J; ++j)
                     if (own[j]) {
 #pragma unroll
-                        for (int e = 0; e < V; ++e) y[j][e] = y[j][e] * sy * wi[j][e];
-                        put(static_cast<T*>(p.h) + n * p.C + c0 + j * cstep, y[j]);
+                        for (int i = 0; i < H; ++i) y[j][i] = mul2(mul2(y[j][i], s1), wi[j][i]);
+                        store2<T, V>(to(p.h, j), y[j]);
                     }
             }
             if (p.stats && threadIdx.x == 0) {
@@ -550,65 +564,66 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
                 if (pre) p.stats[p.N + n] = sy;
             }
         } else {
-            float gx[J][V], gh[J][V];
-            float v = 0.f;
+            F2 gx[J][H], gh[J][H], v(0.f);
+            const F2 s0(sb), s1(sy);
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 if (!own[j]) continue;
-                if (more) lds(gx[j], at(s.o_gx, j));
+                if (more) load2<T, V>(gx[j], at(s.o_gx, j));
                 else
 #pragma unroll
-                    for (int e = 0; e < V; ++e) gx[j][e] = 0.f;
+                    for (int i = 0; i < H; ++i) gx[j][i] = F2(0.f);
                 if (post)
 #pragma unroll
-                    for (int e = 0; e < V; ++e) bs[j][e] *= sb;
+                    for (int i = 0; i < H; ++i) bs[j][i] = mul2(bs[j][i], s0);
                 if (pre) {
-                    lds(gh[j], at(s.o_gh, j));
+                    load2<T, V>(gh[j], at(s.o_gh, j));
 #pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        if (post) y[j][e] = fmaf(sa[j][e] * wo[j][e], bs[j][e], y[j][e]);
-                        const float gy = gh[j][e] * y[j][e];
-                        v = fmaf(gy, wi[j][e], v);
-                        dwi[j][e] = fmaf(gy, sy, dwi[j][e]);
+                    for (int i = 0; i < H; ++i) {
+                        if (post) y[j][i] = fma2(mul2(sa[j][i], wo[j][i]), bs[j][i], y[j][i]);
+                        const F2 gy = mul2(gh[j][i], y[j][i]);
+                        v = fma2(gy, wi[j][i], v);
+                        dwi[j][i] = fma2(gy, s1, dwi[j][i]);
                     }
                 }
             }
-            float m1 = 0.f;
             if (pre) {
-                m1 = sum(v) * inv_m * sy * sy * sy;
+                const F2 m1(-(sum(v.sum()) * inv_m * sy * sy * sy));
                 release();
+                // t, the gradient of x_out in all, in the place of gx
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+                    if (own[j])
+#pragma unroll
+                        for (int i = 0; i < H; ++i)
+                            gx[j][i] = fma2(m1, y[j][i], fma2(gh[j][i], mul2(s1, wi[j][i]), gx[j][i]));
             }
-            v = 0.f;
+            v = F2(0.f);
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 if (!own[j]) continue;
-                // t, the gradient of x_out in all, in the place of gx
-                if (pre)
-#pragma unroll
-                    for (int e = 0; e < V; ++e)
-                        gx[j][e] = fmaf(-m1, y[j][e], fmaf(gh[j][e], sy * wi[j][e], gx[j][e]));
-                put(static_cast<T*>(p.dx) + n * p.C + c0 + j * cstep, gx[j]);
+                store2<T, V>(to(p.dx, j), gx[j]);
                 if (!post) continue;
-                float dg[V];
+                F2 dg[H];
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float tb = gx[j][e] * bs[j][e];
-                    dwo[j][e] = fmaf(sa[j][e], tb, dwo[j][e]);
-                    dg[e] = gated ? p.scale * da[j][e] * wo[j][e] * tb : 0.f;
-                    gx[j][e] *= sa[j][e] * wo[j][e];          // q
-                    v = fmaf(gx[j][e], bs[j][e], v);
+                for (int i = 0; i < H; ++i) {
+                    const F2 tb = mul2(gx[j][i], bs[j][i]);
+                    dwo[j][i] = fma2(sa[j][i], tb, dwo[j][i]);
+                    if (gated) dg[i] = mul2(mul2(da[j][i], scale), mul2(wo[j][i], tb));
+                    gx[j][i] = mul2(gx[j][i], mul2(sa[j][i], wo[j][i]));          // q
+                    v = fma2(gx[j][i], bs[j][i], v);
                 }
-                if (gated) put(static_cast<T*>(p.dgate) + n * p.C + c0 + j * cstep, dg);
+                if (gated) store2<T, V>(to(p.dgate, j), dg);
             }
             if (post) {
-                const float m2 = sum(v) * inv_m;
+                const F2 m2(-(sum(v.sum()) * inv_m));
                 if (!pre) release();
 #pragma unroll
                 for (int j = 0; j < J; ++j)
                     if (own[j]) {
 #pragma unroll
-                        for (int e = 0; e < V; ++e) gx[j][e] = sb * fmaf(-bs[j][e], m2, gx[j][e]);
-                        put(static_cast<T*>(p.db) + n * p.C + c0 + j * cstep, gx[j]);
+                        for (int i = 0; i < H; ++i) gx[j][i] = mul2(s0, fma2(bs[j][i], m2, gx[j][i]));
+                        store2<T, V>(to(p.db, j), gx[j]);
                     }
             }
         }
@@ -622,8 +637,8 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
 #pragma unroll
         for (int j = 0; j < J; ++j)
             if (own[j]) {
-                put(part + c0 + j * cstep, dwo[j]);
-                put(part + p.C + c0 + j * cstep, dwi[j]);
+                store2<float, V>(part + c0 + j * cstep, dwo[j]);
+                store2<float, V>(part + p.C + c0 + j * cstep, dwi[j]);
             }
     }
 }

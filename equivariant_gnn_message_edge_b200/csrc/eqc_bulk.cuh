@@ -28,6 +28,9 @@ __device__ __forceinline__ void copy(void* dst, const void* src, uint32_t bytes,
         : "memory");
 }
 
+// Orders this thread's writes to shared memory before copies issued behind the next barrier.
+__device__ __forceinline__ void fence_writes() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
 // Waits for the phase of `parity`; false after two seconds without it.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
     const uint32_t a = smem_u32(bar);

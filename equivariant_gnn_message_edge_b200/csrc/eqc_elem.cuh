@@ -8,6 +8,8 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <cstring>
+#include <type_traits>
 
 namespace eqc {
 
@@ -72,6 +74,93 @@ struct Pack {
     __device__ __forceinline__ float get(int i) const { return to_float(e[i]); }
     __device__ __forceinline__ void set(int i, float v) { e[i] = from_float<T>(v); }
 };
+
+// Two fp32 values in a 64-bit register pair: one instruction per pair for
+// products and sums, each half rounded as fp32.
+struct F2 {
+    unsigned long long v;
+    __device__ __forceinline__ F2() {}
+    __device__ __forceinline__ F2(float x, float y) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y)); }
+    __device__ __forceinline__ explicit F2(float x) : F2(x, x) {}
+    __device__ __forceinline__ void split(float& x, float& y) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+    __device__ __forceinline__ float sum() const {
+        float x, y;
+        split(x, y);
+        return x + y;
+    }
+};
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return d;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+
+// V elements of shared memory as pairs (p on the vector's boundary, 16 bytes at most), and pairs to memory.
+template <class T, int V>
+__device__ __forceinline__ void load2(F2 (&v)[V / 2], const T* p) {
+    constexpr int kWords = V * (int)sizeof(T) / 4;
+    uint32_t w[kWords];
+    if constexpr (kWords % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < kWords / 4; ++i) {
+            const uint4 q = reinterpret_cast<const uint4*>(p)[i];
+            w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
+        }
+    } else {
+        static_assert(kWords == 2, "8 bytes");
+        const uint2 q = *reinterpret_cast<const uint2*>(p);
+        w[0] = q.x, w[1] = q.y;
+    }
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+        if constexpr (sizeof(T) == 4) {
+            v[i] = F2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+            v[i] = F2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+        } else {
+            __half2 h;
+            memcpy(&h, &w[i], 4);
+            const float2 f = __half22float2(h);
+            v[i] = F2(f.x, f.y);
+        }
+    }
+}
+template <class T, int V>
+__device__ __forceinline__ void store2(T* p, const F2 (&v)[V / 2]) {
+    constexpr int kWords = V * (int)sizeof(T) / 4;
+    uint32_t w[kWords];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+        float x, y;
+        v[i].split(x, y);
+        if constexpr (sizeof(T) == 4) {
+            w[2 * i] = __float_as_uint(x), w[2 * i + 1] = __float_as_uint(y);
+        } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+            memcpy(&w[i], &b, 4);
+        } else {
+            const __half2 h = __floats2half2_rn(x, y);
+            memcpy(&w[i], &h, 4);
+        }
+    }
+    if constexpr (kWords % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < kWords / 4; ++i)
+            reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    } else {
+        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    }
+}
 
 // Bytes of one element of a type code (0: unknown code).
 inline int type_bytes(int code) { return code == 0 ? 4 : (code == 1 || code == 2) ? 2 : 0; }
