@@ -64,9 +64,11 @@ __device__ __forceinline__ float rcp_fast(float x) {
 // a(g) and a'(g) of V gates (pairs), of one kind (EQCONV_GATE_*).  The error is
 // a few units in the last place of fp32, and |g| more of them through the
 // rounded argument of the power.  tanh is (1 - q) / (1 + q) of q = exp(-2 |g|),
-// and near 0, where that cancels, its Taylor series (for |g| < 0.25 the first
-// term left out is below 2^-28 of the value).
-template <int V>
+// and near 0, where that cancels, its Taylor series: for |g| < 0.25 up to a
+// term below 2^-28 of the value.  16-bit gates take g itself below 2^-8, which
+// leaves 2^-17 of the value there and above: 2^-6 of their own type's rounding
+// or less, for a third fewer instructions in rows that these bound.
+template <int V, bool SHORT = false>
 __device__ __forceinline__ void gate_values(int kind, const F2 (&g)[V / 2], F2 (&a)[V / 2], F2 (&da)[V / 2]) {
     constexpr float kLog2e = 1.4426950408889634f;
     const F2 one(1.f), minus(-1.f);
@@ -76,18 +78,23 @@ __device__ __forceinline__ void gate_values(int kind, const F2 (&g)[V / 2], F2 (
             float x, y;
             g[i].split(x, y);
             const float qx = exp2_fast(-2.f * kLog2e * fabsf(x)), qy = exp2_fast(-2.f * kLog2e * fabsf(y));
-            const F2 q(qx, qy), g2 = mul2(g[i], g[i]);
+            const F2 q(qx, qy);
             float nx, ny, dx, dy, sx, sy, fx, fy;
             fma2(q, minus, one).split(nx, ny);
             add2(q, one).split(dx, dy);
-            F2 c = fma2(g2, F2(-1382.f / 155925.f), F2(62.f / 2835.f));
-            c = fma2(g2, c, F2(-17.f / 315.f));
-            c = fma2(g2, c, F2(2.f / 15.f));
-            c = fma2(g2, c, F2(-1.f / 3.f));
-            fma2(mul2(g[i], g2), c, g[i]).split(sx, sy);
             fx = copysignf(nx * rcp_fast(dx), x);
             fy = copysignf(ny * rcp_fast(dy), y);
-            a[i] = F2(fabsf(x) < 0.25f ? sx : fx, fabsf(y) < 0.25f ? sy : fy);
+            if constexpr (SHORT) {
+                a[i] = F2(fabsf(x) < 0x1p-8f ? x : fx, fabsf(y) < 0x1p-8f ? y : fy);
+            } else {
+                const F2 g2 = mul2(g[i], g[i]);
+                F2 c = fma2(g2, F2(-1382.f / 155925.f), F2(62.f / 2835.f));
+                c = fma2(g2, c, F2(-17.f / 315.f));
+                c = fma2(g2, c, F2(2.f / 15.f));
+                c = fma2(g2, c, F2(-1.f / 3.f));
+                fma2(mul2(g[i], g2), c, g[i]).split(sx, sy);
+                a[i] = F2(fabsf(x) < 0.25f ? sx : fx, fabsf(y) < 0.25f ? sy : fy);
+            }
             da[i] = fma2(mul2(a[i], minus), a[i], one);
         }
     } else {

@@ -95,7 +95,7 @@ __device__ __forceinline__ void fwd_node(const BnParams& p, const View<T>& s, co
             if (gated) {
                 F2 g[H], a[H], da[H];
                 load2<T, V>(g, s.g + l * p.C);
-                gate_values<V>(p.gate_kind, g, a, da);
+                gate_values<V, sizeof(T) == 2>(p.gate_kind, g, a, da);
 #pragma unroll
                 for (int i = 0; i < H; ++i) k[l][i] = mul2(k[l][i], a[i]);
             }
@@ -177,7 +177,7 @@ __device__ __forceinline__ void bwd_node(const BnParams& p, const View<T>& s, co
         if (gated) {
             F2 g[H];
             load2<T, V>(g, s.g + l * p.C);
-            gate_values<V>(p.gate_kind, g, sa[l], da[l]);
+            gate_values<V, sizeof(T) == 2>(p.gate_kind, g, sa[l], da[l]);
         }
 #pragma unroll
         for (int i = 0; i < H; ++i) {
@@ -438,10 +438,12 @@ struct CtaSum {
         flip ^= 1;       // the next sum's buffer: one barrier a sum is enough
         if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = v;
         __syncthreads();
-        const float4* q = reinterpret_cast<const float4*>(r);
-        const float4 a = q[0], b = q[1], c = q[2], d = q[3];
-        return ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w)) + ((c.x + c.y) + (c.z + c.w)) +
-               ((d.x + d.y) + (d.z + d.w));
+        F2 q[4][2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load2<float, 4>(q[i], r + 4 * i);
+        return add2(add2(add2(q[0][0], q[0][1]), add2(q[1][0], q[1][1])),
+                    add2(add2(q[2][0], q[2][1]), add2(q[3][0], q[3][1])))
+            .sum();
     }
 };
 
@@ -512,7 +514,7 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
             if (gated) {
                 F2 g[H];
                 load2<T, V>(g, at(s.o_g, j));
-                gate_values<V>(p.gate_kind, g, sa[j], da[j]);
+                gate_values<V, sizeof(T) == 2>(p.gate_kind, g, sa[j], da[j]);
 #pragma unroll
                 for (int i = 0; i < H; ++i) sa[j][i] = mul2(sa[j][i], scale);
             } else {
