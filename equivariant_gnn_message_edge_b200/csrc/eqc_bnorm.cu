@@ -100,18 +100,22 @@ cudaError_t run(BnParams& p, const BlockNormArgs& a, bool bwd, cudaStream_t st, 
         s.node_bytes = (a.L + 1) * (a.L + 1) * a.C * es;
         s.gate_bytes = a.gate ? (a.L + 1) * a.C * es : 0;
         int o = 0;
-        const auto place = [&](bool there) {
+        const auto place = [&](bool there, const void* from, int bytes) {
             const int at = o;
-            if (there) o += s.node_bytes * h.nodes;
+            if (there) {
+                s.from[s.tensors] = static_cast<const unsigned char*>(from);
+                s.bytes[s.tensors] = bytes;
+                s.offset[s.tensors++] = at;
+                o += bytes * h.nodes;
+            }
             return at;
         };
-        s.o_x = place(!bwd || a.g_h);
-        s.o_b = place(a.b);
-        s.o_gx = place(bwd && a.g_x);
-        s.o_gh = place(bwd && a.g_h);
-        s.o_g = o;
-        s.slot_bytes = o + s.gate_bytes * h.nodes;
-        s.per_node = s.slot_bytes / h.nodes;
+        s.o_x = place(!bwd || a.g_h, a.x, s.node_bytes);
+        s.o_b = place(a.b, a.b, s.node_bytes);
+        s.o_gx = place(bwd && a.g_x, a.g_x, s.node_bytes);
+        s.o_gh = place(bwd && a.g_h, a.g_h, s.node_bytes);
+        s.o_g = place(a.gate, a.gate, s.gate_bytes);
+        s.slot_bytes = o;
         s.status = a.status;
         const int64_t most = (int64_t)kSMs * h.ctas;
         const int grid = (int)(s.total < most ? s.total : most);

@@ -23,34 +23,30 @@ struct StagedParams {
     BnParams p;
     int slots, nodes;          // slots of the ring, nodes a slot
     int64_t total;             // slots' worth of nodes in all
-    // byte offsets of the tensors in a slot, and their bytes a node
-    int o_x, o_b, o_gx, o_gh, o_g, slot_bytes, node_bytes, gate_bytes, per_node;
+    // the tensors of a slot: where they come from, their bytes a node, their place in the slot
+    int tensors;
+    const unsigned char* from[5];
+    int bytes[5], offset[5];
+    int o_x, o_b, o_gx, o_gh, o_g, slot_bytes, node_bytes, gate_bytes;
     unsigned* status;
 };
 
 struct Ring {
     unsigned char* base;
-    uint64_t* full;
+    uint64_t* full;            // a phase: one arrival per tensor, and its bytes
 };
 
-// Copies of sequence number k of this CTA into its slot, by one thread.
-template <bool BWD>
-__device__ __forceinline__ void fill(const StagedParams& s, const Ring& r, int k) {
+// Copies of sequence number k of this CTA into its slot: tensor t by lane t,
+// so that the warp that does it is held up by one copy's instructions only.
+__device__ __forceinline__ void fill(const StagedParams& s, const Ring& r, int k, int lane) {
     const int64_t g = blockIdx.x + (int64_t)k * gridDim.x;
-    if (g >= s.total) return;
+    if (g >= s.total || lane >= s.tensors) return;
     const int64_t n0 = g * s.nodes;
-    const uint32_t nodes = (uint32_t)(s.p.N - n0 < s.nodes ? s.p.N - n0 : s.nodes);
+    const uint32_t nodes = (uint32_t)(s.p.N - n0 < s.nodes ? s.p.N - n0 : s.nodes), bytes = nodes * s.bytes[lane];
     const int slot = k % s.slots;
-    unsigned char* d = r.base + (int64_t)slot * s.slot_bytes;
-    uint64_t* bar = r.full + slot;
-    bulk::expect(bar, nodes * (uint32_t)s.per_node);
-    const uint32_t nb = nodes * s.node_bytes;
-    const auto from = [&](const void* p, int64_t bytes) { return static_cast<const unsigned char*>(p) + n0 * bytes; };
-    if (!BWD || s.p.g_h) bulk::copy(d + s.o_x, from(s.p.x, s.node_bytes), nb, bar);
-    if (s.p.b) bulk::copy(d + s.o_b, from(s.p.b, s.node_bytes), nb, bar);
-    if (BWD && s.p.g_x) bulk::copy(d + s.o_gx, from(s.p.g_x, s.node_bytes), nb, bar);
-    if (BWD && s.p.g_h) bulk::copy(d + s.o_gh, from(s.p.g_h, s.node_bytes), nb, bar);
-    if (s.p.gate) bulk::copy(d + s.o_g, from(s.p.gate, s.gate_bytes), nodes * s.gate_bytes, bar);
+    bulk::expect(r.full + slot, bytes);
+    bulk::copy(r.base + (int64_t)slot * s.slot_bytes + s.offset[lane], s.from[lane] + n0 * s.bytes[lane], bytes,
+               r.full + slot);
 }
 
 // What one thread sees of its node: the tensors' slot parts at its channels.
@@ -320,7 +316,7 @@ __global__ void __launch_bounds__(256, 1) bn_staged_kernel(const StagedParams s)
     const int sub = CTA ? 0 : lane / width, x0 = lane - sub * width;
     const int c0 = x0 * V;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < s.slots; ++i) bulk::init(full + i);
+        for (int i = 0; i < s.slots; ++i) bulk::init(full + i, s.tensors);
         bulk::fence_init();
     }
     for (int i = threadIdx.x; i < (L + 1) * p.C; i += blockDim.x) {
@@ -328,8 +324,8 @@ __global__ void __launch_bounds__(256, 1) bn_staged_kernel(const StagedParams s)
         w[(L + 1) * p.C + i] = p.w_pre ? p.w_pre[i] : 0.f;
     }
     __syncthreads();
-    if (threadIdx.x == 0)
-        for (int k = 0; k < s.slots; ++k) fill<BWD>(s, ring, k);
+    if (threadIdx.x < 32)
+        for (int k = 0; k < s.slots; ++k) fill(s, ring, k, threadIdx.x);
     const bool own = c0 < p.C;
     F2 dwo[BWD ? L + 1 : 1][V / 2], dwi[BWD ? L + 1 : 1][V / 2];
 #pragma unroll
@@ -381,7 +377,7 @@ __global__ void __launch_bounds__(256, 1) bn_staged_kernel(const StagedParams s)
         if constexpr (BWD && sizeof(T) == 4) bulk::fence_writes();
         if constexpr (CTA) __syncthreads();
         else __syncwarp();
-        if (lane == 0) fill<BWD>(s, ring, k + s.slots);
+        if (lane < 32) fill(s, ring, k + s.slots, lane);
     }
     if (!ok) {
         // the copies still in flight end before the CTA's memory does (each wait is bounded)
@@ -460,12 +456,12 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
     const float inv_m = 1.f / (float)p.C;
     if (threadIdx.x < 32) red[threadIdx.x] = 0.f;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < s.slots; ++i) bulk::init(full + i);
+        for (int i = 0; i < s.slots; ++i) bulk::init(full + i, s.tensors);
         bulk::fence_init();
     }
     __syncthreads();
-    if (threadIdx.x == 0)
-        for (int k = 0; k < s.slots; ++k) fill<BWD>(s, ring, k);
+    if (threadIdx.x < 32)
+        for (int k = 0; k < s.slots; ++k) fill(s, ring, k, threadIdx.x);
     constexpr int H = V / 2;
     bool own[J];
     F2 wo[J][H], wi[J][H], dwo[J][H], dwi[J][H];
@@ -502,7 +498,7 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
         const auto at = [&](int o, int j) { return reinterpret_cast<const T*>(base + o) + c0 + j * cstep; };
         const auto to = [&](void* q, int j) { return static_cast<T*>(q) + n * p.C + c0 + j * cstep; };
         const auto release = [&] {       // behind a barrier: every thread has read the slot
-            if (threadIdx.x == 0) fill<BWD>(s, ring, k + s.slots);
+            if (threadIdx.x < 32) fill(s, ring, k + s.slots, threadIdx.x);
         };
         // y: x, then x_out; bs: b, then b / rms(b); sa, da: scale a(gate), scale a'(gate)
         F2 y[J][H], bs[J][H], sa[J][H], da[J][H];
