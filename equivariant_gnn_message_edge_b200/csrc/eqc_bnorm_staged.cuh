@@ -6,7 +6,7 @@
 // loads, sums and stores follow one another in each warp).  Used where the
 // tensors are 16-byte aligned, C is whole 16-byte vectors and two slots fit.
 //
-// A worker is a warp (32 / width nodes a slot, several workers share the ring)
+// A worker is a warp (32 / width nodes a slot, each warp with slots of its own)
 // or, for wide nodes, the whole CTA (one node a slot).  Its threads own V
 // neighbouring channels of every row of the node.
 #pragma once
@@ -302,10 +302,10 @@ __device__ __forceinline__ void bwd_node(const BnParams& p, const View<T>& s, co
 
 // Shared memory: [w_post, w_pre: 2 (L + 1) C floats] [ring of slots].
 template <class T, int V, int L, bool BWD, bool CTA>
-__global__ void __launch_bounds__(256, 1) bn_staged_kernel(const StagedParams s) {
+__global__ void __launch_bounds__(CTA ? 256 : BWD ? 256 : 512, 1) bn_staged_kernel(const StagedParams s) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ uint64_t full[kMaxSlots];
-    __shared__ float red[2 * (L + 1) * 16];
+    __shared__ float red[CTA ? 2 * (L + 1) * 16 : 1];
     constexpr int D = (L + 1) * (L + 1);
     const BnParams& p = s.p;
     float* w = reinterpret_cast<float*>(smem);
@@ -647,8 +647,7 @@ struct Staged {
     bool row;          // the kernel for wide rows
 };
 
-// Two slots at least, of what an SM's shared memory holds; workers that leave
-// two fifths of the slots to the copies in flight.
+// Two slots at least, of what an SM's shared memory holds.
 inline Staged staged_shape(int L, int C, int es, int tensors, bool gated, bool bwd) {
     Staged s{};
     const int room = 224 * 1024, wbytes = 2 * (L + 1) * C * 4;
@@ -665,8 +664,13 @@ inline Staged staged_shape(int L, int C, int es, int tensors, bool gated, bool b
         const int64_t fit = (room - wbytes) / (node * s.nodes);
         s.slots = (int)(fit < kMaxSlots ? fit : kMaxSlots);
         if (s.slots < 2) return Staged{};
-        int warps = s.slots * 3 / 5;
-        warps = warps < 1 ? 1 : warps > 8 ? 8 : warps;
+        // Every warp has slots of its own (the slots are a multiple of the warps): a slot's next copies are then
+        // waited for by the warp that issued them, so no warp can meet a slot two phases behind, whose barrier would
+        // show the parity of the phase it wants.
+        // One slot a warp is best where that gives no more than 8 warps backward (222 registers a thread; lmax2: 8
+        // slots of 8 warps 170 us, 10 of 5 warps 219 us) or 16 forward (108 us; 16 slots of 8 warps 109 us).
+        const int most = bwd ? 8 : 16, warps = s.slots < most ? s.slots : most;
+        s.slots = s.slots / warps * warps;
         s.threads = 32 * warps;
         // the reduction of the weight gradients takes threads * V floats of the ring
         if ((int64_t)s.slots * s.nodes * node < (int64_t)s.threads * s.V * 4) return Staged{};

@@ -243,6 +243,9 @@ NORM = [  # N, L, C, dtype, gate
     (2, 0, 16384, "bf16", "none"),
     (2000, 1, 16, "fp32", "sigmoid"),
     (4000, 0, 96, "bf16", "silu"),
+    (6001, 2, 128, "fp32", "silu"),          # dozens of nodes for every warp of every SM
+    (5003, 0, 2048, "bf16", "tanh"),
+    (20011, 1, 8, "fp16", "sigmoid"),
 ]
 
 
