@@ -39,12 +39,16 @@ __global__ void __launch_bounds__(256) embed_fwd_kernel(const void* ids, int64_t
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
         const int64_t i = row0 + (int64_t)k * ly;
-        id[k] = i < N ? id_at<ID>(ids, i) : -1;
-        if (i < N && (uint64_t)id[k] >= (uint64_t)V) {
-            id[k] = -1;
-            if (x == 0) atomicOr(status, 1u);
-        }
+        id[k] = i < N ? id_at<ID>(ids, i) : 0;
     }
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < kRows; ++k)
+        if ((uint64_t)id[k] >= (uint64_t)V) {
+            id[k] = -1;
+            bad = true;
+        }
+    if (bad && x == 0) atomicOr(status, 1u);
     for (int c = (blockIdx.y * lx + x) * VE; c < C; c += gridDim.y * lx * VE) {
         Pack<T, VE> in[kRows];
 #pragma unroll
@@ -69,22 +73,49 @@ __global__ void __launch_bounds__(256) embed_fwd_kernel(const void* ids, int64_t
 // row per tile, which a second kernel adds in tile order.  Ids that give no
 // gradient (padding, out of range) get the key V and come last.
 
-template <class ID>
-__device__ __forceinline__ int key_of(const void* ids, int64_t i, int64_t V, int64_t padding, unsigned* status) {
-    const int64_t id = id_at<ID>(ids, i);
-    const bool ok = (uint64_t)id < (uint64_t)V;
-    if (!ok) atomicOr(status, 1u);
-    return ok && id != padding ? (int)id : (int)V;
+// Keys of K nodes, `first` + k `step` below `end`: from the ids, or (FIRST
+// false) as an earlier pass left them.  All loads go out together; bad ids are
+// looked for afterwards.
+template <class ID, bool FIRST, int K>
+__device__ __forceinline__ void load_keys(const void* in, int64_t first, int step, int64_t end, int64_t V,
+                                          int64_t padding, unsigned* status, int (&key)[K]) {
+    if constexpr (FIRST) {
+        int64_t id[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) id[k] = first + k * step < end ? id_at<ID>(in, first + k * step) : 0;
+        bool bad = false;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const bool ok = (uint64_t)id[k] < (uint64_t)V;
+            bad |= !ok;
+            key[k] = ok && id[k] != padding ? (int)id[k] : (int)V;
+        }
+        if (bad) atomicOr(status, 1u);
+    } else {
+#pragma unroll
+        for (int k = 0; k < K; ++k) key[k] = first + k * step < end ? static_cast<const int*>(in)[first + k * step] : 0;
+    }
 }
 
 constexpr int kDigitBits = 9;                 // radix of one sorting pass: at most 512
 constexpr int kRadix = 1 << kDigitBits;
 
+// The lanes that hold the same digit (by one vote per bit), among the valid.
+__device__ __forceinline__ unsigned same_digit(int d, int bits, bool valid) {
+    unsigned peers = __ballot_sync(0xffffffffu, valid);
+    for (int b = 0; b < bits; ++b) {
+        const bool one = (d >> b) & 1;
+        const unsigned m = __ballot_sync(0xffffffffu, one);
+        peers &= one ? m : ~m;
+    }
+    return peers;
+}
+
 // Ranks a warp's 32 keys of one round by digit, stably, behind the keys that
 // the warp ranked in earlier rounds (counted in h[digit]).
-__device__ __forceinline__ int warp_rank(int* h, int d, bool valid) {
+__device__ __forceinline__ int warp_rank(int* h, int d, int bits, bool valid) {
     const int lane = threadIdx.x & 31;
-    const unsigned peers = __match_any_sync(0xffffffffu, valid ? d : kRadix + lane);
+    const unsigned peers = same_digit(d, bits, valid);
     const int before = __popc(peers & ((1u << lane) - 1u));
     const int rank = valid ? h[d] + before : 0;
     __syncwarp();
@@ -105,9 +136,11 @@ __device__ __forceinline__ int block_exclusive(int v, int* warp_sums) {
     }
     if (lane == 31) warp_sums[warp] = inc;
     __syncthreads();
-    int off = 0;
-    for (int w = 0; w < warp; ++w) off += warp_sums[w];
-    return off + inc - v;
+    // every warp adds up the sums of the warps before it
+    int before = lane < warp ? warp_sums[lane] : 0;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+    return before + inc - v;
 }
 
 // Sort of up to 8 x 8192 nodes in one launch by one cluster: keys and node
@@ -116,76 +149,100 @@ __device__ __forceinline__ int block_exclusive(int v, int* warp_sums) {
 // by latency; the launch it saves per step is worth more than its idle SMs.
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortRounds = 8;
-constexpr int kSortCap = kSortThreads * kSortRounds;
+constexpr int kSortCap = kSortThreads * 8;
 constexpr int kMaxCluster = 8;
 
+// ROUNDS (1, 2, 4, 8): nodes a thread.
+template <int ROUNDS>
 struct SortSmem {
-    int key[2][kSortCap];
-    int idx[2][kSortCap];
+    int key[2][kSortThreads * ROUNDS];
+    int idx[2][kSortThreads * ROUNDS];
     int hist[kSortWarps][kRadix];
     int total[kRadix];
     int base[kRadix];
     int warp_sums[kSortWarps];
 };
 
-template <class ID>
+template <class ID, int ROUNDS>
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const void* ids, int N, int64_t V, int64_t padding,
-                                                                  int rounds_log2, int digit_bits, int passes,
-                                                                  int* keys, int* perm, unsigned* status) {
+                                                                  int digit_bits, int passes, int* keys, int* perm,
+                                                                  uint4* zero, int64_t zeros, unsigned* status) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    SortSmem& s = *reinterpret_cast<SortSmem*>(smem_raw);
+    SortSmem<ROUNDS>& s = *reinterpret_cast<SortSmem<ROUNDS>*>(smem_raw);
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
+    if ((int)blockIdx.x >= ctas) {
+        // the other SMs write zeros to the first rows of the table meanwhile
+        for (int64_t i = (int64_t)(blockIdx.x - ctas) * kSortThreads + threadIdx.x; i < zeros;
+             i += (int64_t)(gridDim.x - ctas) * kSortThreads)
+            zero[i] = make_uint4(0, 0, 0, 0);
+        return;
+    }
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rounds = 1 << rounds_log2, cap_log2 = 10 + rounds_log2, cap = 1 << cap_log2;
+    constexpr int cap = kSortThreads * ROUNDS;
     const int radix = 1 << digit_bits;
-    const int first = warp * 32 * rounds + lane;       // this thread's items: first + 32 k
-    for (int k = 0; k < rounds; ++k) {
-        const int j = first + 32 * k, i = rank * cap + j;
-        if (i < N) {
-            s.key[0][j] = key_of<ID>(ids, i, V, padding, status);
-            s.idx[0][j] = i;
+    const int first = warp * 32 * ROUNDS + lane;       // this thread's items: first + 32 k
+    {
+        int key[ROUNDS];
+        load_keys<ID, true>(ids, rank * cap + first, 32, N, V, padding, status, key);
+#pragma unroll
+        for (int k = 0; k < ROUNDS; ++k) {
+            s.key[0][first + 32 * k] = key[k];
+            s.idx[0][first + 32 * k] = rank * cap + first + 32 * k;
         }
     }
     for (int p = 0; p < passes; ++p) {
         const int shift = p * digit_bits, cur = p & 1;
-        int key[kSortRounds], at[kSortRounds];
+        int key[ROUNDS], at[ROUNDS];
         for (int d = lane; d < radix; d += 32) s.hist[warp][d] = 0;
         __syncwarp();
 #pragma unroll
-        for (int k = 0; k < kSortRounds; ++k) {
-            if (k >= rounds) break;
+        for (int k = 0; k < ROUNDS; ++k) {
             const int j = first + 32 * k;
             const bool valid = rank * cap + j < N;
             key[k] = valid ? s.key[cur][j] : 0;
-            at[k] = warp_rank(s.hist[warp], (key[k] >> shift) & (radix - 1), valid);
+            at[k] = warp_rank(s.hist[warp], (key[k] >> shift) & (radix - 1), digit_bits, valid);
         }
         __syncthreads();
-        if (tid < radix) {
-            int run = 0;
-#pragma unroll 8
-            for (int w = 0; w < kSortWarps; ++w) {
-                const int c = s.hist[w][tid];
-                s.hist[w][tid] = run;
-                run += c;
+        // the warps' counts of a digit become their first ranks: two threads a digit, half of the warps each
+        const int half = tid >> kDigitBits, d0 = tid & (kRadix - 1);
+        int count[kSortWarps / 2], sum = 0;
+        if (d0 < radix) {
+#pragma unroll
+            for (int w = 0; w < kSortWarps / 2; ++w) count[w] = s.hist[half * (kSortWarps / 2) + w][d0];
+#pragma unroll
+            for (int w = 0; w < kSortWarps / 2; ++w) {
+                const int c = count[w];
+                count[w] = sum;
+                sum += c;
             }
-            s.total[tid] = run;
+            if (half == 0) s.base[d0] = sum;
+        }
+        __syncthreads();
+        if (d0 < radix) {
+            const int off = half ? s.base[d0] : 0;
+#pragma unroll
+            for (int w = 0; w < kSortWarps / 2; ++w) s.hist[half * (kSortWarps / 2) + w][d0] = off + count[w];
+            if (half) s.total[d0] = off + sum;
         }
         cluster.sync();
         int all = 0, below = 0;
-        if (tid < radix)
-            for (int q = 0; q < ctas; ++q) {
-                const int c = *cluster.map_shared_rank(&s.total[tid], q);
-                all += c;
-                if (q < rank) below += c;
+        if (tid < radix) {
+            int c[kMaxCluster];
+#pragma unroll
+            for (int q = 0; q < kMaxCluster; ++q)
+                c[q] = q < ctas ? *cluster.map_shared_rank(&s.total[tid], q) : 0;
+#pragma unroll
+            for (int q = 0; q < kMaxCluster; ++q) {
+                all += c[q];
+                if (q < rank) below += c[q];
             }
+        }
         const int excl = block_exclusive<kSortThreads>(all, s.warp_sums);
         if (tid < radix) s.base[tid] = excl + below;
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < kSortRounds; ++k) {
-            if (k >= rounds) break;
+        for (int k = 0; k < ROUNDS; ++k) {
             const int j = first + 32 * k;
             if (rank * cap + j >= N) continue;
             const int d = (key[k] >> shift) & (radix - 1);
@@ -194,7 +251,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const void* id
                 keys[pos] = key[k];
                 perm[pos] = idx;
             } else {
-                const int q = pos >> cap_log2, o = pos & (cap - 1);
+                const int q = pos / cap, o = pos % cap;
                 *cluster.map_shared_rank(&s.key[cur ^ 1][o], q) = key[k];
                 *cluster.map_shared_rank(&s.idx[cur ^ 1][o], q) = idx;
             }
@@ -208,14 +265,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const void* id
 constexpr int kLsdThreads = 512;
 constexpr int kLsdRounds = 8;
 constexpr int kLsdTile = kLsdThreads * kLsdRounds;
-static_assert(kLsdThreads == kRadix, "one thread per digit");
-
-// The key of node i of a pass: from the ids (first pass), or from the last pass.
-template <class ID, bool FIRST>
-__device__ __forceinline__ int pass_key(const void* in, int64_t i, int64_t V, int64_t padding, unsigned* status) {
-    if constexpr (FIRST) return key_of<ID>(in, i, V, padding, status);
-    else return static_cast<const int*>(in)[i];
-}
+static_assert(kLsdThreads == kRadix && kSortThreads == 2 * kRadix, "one and two threads per digit");
 
 template <class ID, bool FIRST>
 __global__ void __launch_bounds__(kLsdThreads) embed_hist_kernel(const void* in, int N, int64_t V, int64_t padding,
@@ -225,13 +275,14 @@ __global__ void __launch_bounds__(kLsdThreads) embed_hist_kernel(const void* in,
     h[threadIdx.x] = 0;
     __syncthreads();
     const int64_t i0 = (int64_t)blockIdx.x * kLsdTile + threadIdx.x;
+    int key[kLsdRounds];
+    load_keys<ID, FIRST>(in, i0, kLsdThreads, N, V, padding, status, key);
 #pragma unroll
     for (int k = 0; k < kLsdRounds; ++k) {
-        const int64_t i = i0 + k * kLsdThreads;
-        const bool valid = i < N;
-        const int d = valid ? (pass_key<ID, FIRST>(in, i, V, padding, status) >> shift) & mask : 0;
+        const bool valid = i0 + k * kLsdThreads < N;
+        const int d = (key[k] >> shift) & mask;
         // lanes with one digit count it once: a table of few types would serialise on it
-        const unsigned peers = __match_any_sync(0xffffffffu, valid ? d : kRadix + (threadIdx.x & 31));
+        const unsigned peers = same_digit(d, 32 - __clz(mask), valid);
         if (valid && __ffs(peers) - 1 == (int)(threadIdx.x & 31)) atomicAdd(&h[d], __popc(peers));
     }
     __syncthreads();
@@ -273,13 +324,13 @@ __global__ void __launch_bounds__(kLsdThreads) embed_scatter_kernel(const void* 
     __syncwarp();
     const int64_t i0 = (int64_t)blockIdx.x * kLsdTile + warp * 32 * kLsdRounds + lane;
     int key[kLsdRounds], at[kLsdRounds];
+    load_keys<ID, FIRST>(in, i0, 32, N, V, padding, status, key);
+    int idx[kLsdRounds];
 #pragma unroll
-    for (int k = 0; k < kLsdRounds; ++k) {
-        const bool valid = i0 + 32 * k < N;
-        key[k] = valid ? pass_key<ID, FIRST>(in, i0 + 32 * k, V, padding, status) : 0;
-    }
+    for (int k = 0; k < kLsdRounds; ++k)
+        idx[k] = FIRST ? (int)(i0 + 32 * k) : i0 + 32 * k < N ? idx_in[i0 + 32 * k] : 0;
 #pragma unroll
-    for (int k = 0; k < kLsdRounds; ++k) at[k] = warp_rank(wh[warp], (key[k] >> shift) & mask, i0 + 32 * k < N);
+    for (int k = 0; k < kLsdRounds; ++k) at[k] = warp_rank(wh[warp], (key[k] >> shift) & mask, 32 - __clz(mask), i0 + 32 * k < N);
     __syncthreads();
     if (tid <= mask) {
         int run = base[tid];
@@ -297,15 +348,20 @@ __global__ void __launch_bounds__(kLsdThreads) embed_scatter_kernel(const void* 
         if (i >= N) continue;
         const int pos = wh[warp][(key[k] >> shift) & mask] + at[k];
         keys_out[pos] = key[k];
-        idx_out[pos] = FIRST ? (int)i : idx_in[i];
+        idx_out[pos] = idx[k];
     }
 }
+
+// Rows of a block that writes zeros: 512 KB of them, so that the search takes
+// little of its time, and at most 2048.
+constexpr int kZeroRows = 2048, kZeroBytes = 512 * 1024;
+constexpr int64_t kSortZeroBytes = 96 << 20;
 
 struct SumParams {
     const int *keys, *perm;   // nodes in type order
     int N, C, R, tiles, slabs, lx_log2;
     int sum_blocks, zero_rows;
-    int64_t V, ldg;
+    int64_t V, ldg, zero_from;     // rows up to zero_from are zeros already
     float scale;
     float* part;              // [tiles][2][C]: the type begun before the tile, the one that goes on behind it
 };
@@ -327,12 +383,12 @@ __device__ __forceinline__ int lower_bound(const int* keys, int n, int k) {
 template <class T, class O, int VE>
 __global__ void __launch_bounds__(256) embed_sum_kernel(const SumParams p, const O* gy, T* dtable) {
     if ((int)blockIdx.x >= p.sum_blocks) {
-        __shared__ bool empty[256];
-        const int64_t v0 = (int64_t)(blockIdx.x - p.sum_blocks) * p.zero_rows;
+        __shared__ bool empty[kZeroRows];
+        const int64_t v0 = p.zero_from + (int64_t)(blockIdx.x - p.sum_blocks) * p.zero_rows;
         const int rows = (int)(p.V - v0 < p.zero_rows ? p.V - v0 : p.zero_rows);
-        if ((int)threadIdx.x < rows) {
-            const int v = (int)(v0 + threadIdx.x), at = lower_bound(p.keys, p.N, v);
-            empty[threadIdx.x] = at >= p.N || p.keys[at] != v;
+        for (int r = threadIdx.x; r < rows; r += 256) {
+            const int v = (int)(v0 + r), at = lower_bound(p.keys, p.N, v);
+            empty[r] = at >= p.N || p.keys[at] != v;
         }
         __syncthreads();
         Pack<T, VE> zero;
@@ -416,7 +472,12 @@ __global__ void __launch_bounds__(256) embed_join_kernel(const SumParams p, T* d
     const int k = __ldg(p.keys + end - 1);
     if (k == (int)p.V || __ldg(p.keys + end) != k) return;
     if (tile > 0 && __ldg(p.keys + end - p.R - 1) == k) return;      // begun in an earlier tile
-    const int last = (lower_bound(p.keys, p.N, k + 1) - 1) / p.R;     // tile of the type's last node
+    // tile of the type's last node: the tiles behind that begin with the type follow one another
+    int last = tile;
+    for (int more = 256; more == 256; last += more) {
+        const int64_t at = (int64_t)(last + 1 + threadIdx.x) * p.R;
+        more = __syncthreads_count(at < p.N && __ldg(p.keys + at) == k);
+    }
     const int lanes = 1 << p.lx_log2, workers = 256 >> p.lx_log2;
     const int x = threadIdx.x & (lanes - 1), w = threadIdx.x >> p.lx_log2;
     const int c = ((slab << p.lx_log2) + x) * VE;
@@ -433,7 +494,7 @@ __global__ void __launch_bounds__(256) embed_join_kernel(const SumParams p, T* d
 #pragma unroll
             for (int e = 0; e < VE; ++e) acc[e] = v.e[e];
         }
-#pragma unroll 4
+#pragma unroll 8
         for (int t = t0; t < t1; ++t) {
             Pack<float, VE> v;
             v.load(p.part + (int64_t)t * 2 * p.C + c);
@@ -558,19 +619,16 @@ EmbedWs embed_layout(int C, int64_t N) {
     return w;
 }
 
-template <class ID>
-cudaError_t sort_in_cluster(const EmbedArgs& a, int digit_bits, int passes, int* keys, int* perm, cudaStream_t st) {
-    // one CTA up to 4096 nodes, then clusters of 2, 4 and 8
-    int ctas = 1, rounds_log2 = 0;
-    while (ctas < kMaxCluster && a.N > (int64_t)ctas * 4096) ctas *= 2;
-    while (((int64_t)ctas * kSortThreads << rounds_log2) < a.N) ++rounds_log2;
+template <class ID, int ROUNDS>
+cudaError_t launch_sort(const EmbedArgs& a, int ctas, int digit_bits, int passes, int* keys, int* perm,
+                        void* dtable, int64_t zeros, cudaStream_t st) {
     static bool done[64] = {};
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
     if (dev < 0 || dev >= 64 || !done[dev]) {
-        err = cudaFuncSetAttribute(embed_sort_kernel<ID>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   (int)sizeof(SortSmem));
+        err = cudaFuncSetAttribute(embed_sort_kernel<ID, ROUNDS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   (int)sizeof(SortSmem<ROUNDS>));
         if (err != cudaSuccess) return err;
         if (dev >= 0 && dev < 64) done[dev] = true;
     }
@@ -579,16 +637,29 @@ cudaError_t sort_in_cluster(const EmbedArgs& a, int digit_bits, int passes, int*
     attr.val.clusterDim.x = ctas;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ctas);
+    cfg.gridDim = dim3(zeros ? 148 / ctas * ctas : ctas);
     cfg.blockDim = dim3(kSortThreads);
-    cfg.dynamicSmemBytes = sizeof(SortSmem);
+    cfg.dynamicSmemBytes = sizeof(SortSmem<ROUNDS>);
     cfg.stream = st;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    err = cudaLaunchKernelEx(&cfg, embed_sort_kernel<ID>, a.ids, (int)a.N, a.V, a.padding, rounds_log2, digit_bits,
-                             passes, keys, perm, a.status);
+    err = cudaLaunchKernelEx(&cfg, embed_sort_kernel<ID, ROUNDS>, a.ids, (int)a.N, a.V, a.padding, digit_bits, passes,
+                             keys, perm, static_cast<uint4*>(dtable), zeros, a.status);
     count_launch();
     return err;
+}
+
+// One CTA up to 1024 nodes, clusters of 2, 4 and 8 up to 8192, then more nodes a thread.
+template <class ID>
+cudaError_t sort_in_cluster(const EmbedArgs& a, int digit_bits, int passes, int* keys, int* perm, void* dtable,
+                            int64_t zeros, cudaStream_t st) {
+    int ctas = 1;
+    while (ctas < kMaxCluster && a.N > (int64_t)ctas * kSortThreads) ctas *= 2;
+    const int64_t rounds = (a.N + (int64_t)ctas * kSortThreads - 1) / ((int64_t)ctas * kSortThreads);
+    if (rounds <= 1) return launch_sort<ID, 1>(a, ctas, digit_bits, passes, keys, perm, dtable, zeros, st);
+    if (rounds <= 2) return launch_sort<ID, 2>(a, ctas, digit_bits, passes, keys, perm, dtable, zeros, st);
+    if (rounds <= 4) return launch_sort<ID, 4>(a, ctas, digit_bits, passes, keys, perm, dtable, zeros, st);
+    return launch_sort<ID, 8>(a, ctas, digit_bits, passes, keys, perm, dtable, zeros, st);
 }
 
 template <class ID>
@@ -640,12 +711,22 @@ cudaError_t embed_backward(const EmbedArgs& a, const void* gy, int64_t gy_stride
     // keys 0..V in equal digits of at most 9 bits
     const int bits = bit_length(a.V), passes = cdiv(bits, kDigitBits), digit_bits = cdiv(bits, passes);
     cudaError_t err;
-    if (a.N <= (int64_t)kMaxCluster * kSortCap)
-        err = a.id_bits == 32 ? sort_in_cluster<int32_t>(a, digit_bits, passes, keys, perm, st)
-                              : sort_in_cluster<int64_t>(a, digit_bits, passes, keys, perm, st);
-    else
+    // A sort of one cluster leaves the other SMs idle for some 10 us: they write zeros to the first rows meanwhile
+    // (whole 16 bytes, up to 96 MB), and the sums overwrite those that have nodes.
+    int64_t zero_to = 0;
+    const int64_t row = (int64_t)a.C * type_bytes(a.in_type);
+    if (a.N <= (int64_t)kMaxCluster * kSortCap) {
+        if (reinterpret_cast<uintptr_t>(dtable) % 16 == 0) {
+            zero_to = kSortZeroBytes / row;
+            zero_to = (zero_to < a.V ? zero_to : a.V) / 16 * 16;
+        }
+        const int64_t zeros = zero_to * row / 16;
+        err = a.id_bits == 32 ? sort_in_cluster<int32_t>(a, digit_bits, passes, keys, perm, dtable, zeros, st)
+                              : sort_in_cluster<int64_t>(a, digit_bits, passes, keys, perm, dtable, zeros, st);
+    } else {
         err = a.id_bits == 32 ? sort_in_tiles<int32_t>(a, digit_bits, passes, base, w, &keys, &perm, st)
                               : sort_in_tiles<int64_t>(a, digit_bits, passes, base, w, &keys, &perm, st);
+    }
     if (err != cudaSuccess) return err;
     return with_type(a.in_type, [&](auto tv) {
         using T = decltype(tv);
@@ -668,9 +749,10 @@ cudaError_t embed_backward(const EmbedArgs& a, const void* gy, int64_t gy_stride
                 p.scale = a.scale;
                 p.part = reinterpret_cast<float*>(base + w.part);
                 p.sum_blocks = cdiv(((int64_t)s.tiles * s.slabs) << s.lx_log2, 256);
-                const int64_t row = (int64_t)a.C * sizeof(T), zr = 65536 / row;      // 64 KB of rows a block
-                p.zero_rows = (int)(zr < 1 ? 1 : zr > 256 ? 256 : zr);
-                embed_sum_kernel<T, O, VE><<<p.sum_blocks + cdiv(a.V, p.zero_rows), 256, 0, st>>>(
+                const int64_t zr = kZeroBytes / row;
+                p.zero_from = zero_to;
+                p.zero_rows = (int)(zr < 1 ? 1 : zr > kZeroRows ? kZeroRows : zr);
+                embed_sum_kernel<T, O, VE><<<p.sum_blocks + cdiv(a.V - zero_to, p.zero_rows), 256, 0, st>>>(
                     p, static_cast<const O*>(gy), static_cast<T*>(dtable));
                 count_launch();
                 if (s.tiles > 1) {
