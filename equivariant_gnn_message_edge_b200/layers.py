@@ -16,7 +16,10 @@ and take the gradients with torch.autograd.grad.
 """
 from __future__ import annotations
 
+import array
 import contextlib
+import functools
+import itertools
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -27,6 +30,12 @@ _TYPES = {torch.float32: B.EQCONV_F32, torch.bfloat16: B.EQCONV_BF16, torch.floa
 _GATES = {"none": B.EQCONV_GATE_NONE, "sigmoid": B.EQCONV_GATE_SIGMOID, "silu": B.EQCONV_GATE_SILU,
           "tanh": B.EQCONV_GATE_TANH}
 _NOTHING = contextlib.nullcontext()
+_KINDS = {torch.Tensor, torch.nn.Parameter}
+
+
+@functools.lru_cache(None)
+def _device(index: int):
+    return torch.device("cuda", index)
 
 
 def _type_code(dtype) -> int:
@@ -47,17 +56,24 @@ def _on(device: int, stream):
 
 
 def _check(name, t, shape, dtype, device: int):
+    """The tensor's address, if it is what the operator takes."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and t.shape == shape and \
+            t.is_contiguous():
+        return t.data_ptr()
+    _refuse(name, t, shape, dtype, device)
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _refuse(name, t, shape, dtype, device: int):
+    """Raises what is wrong with a tensor's kind, place, type or shape, if anything is."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a CUDA tensor, got {type(t)}")
-    if not t.is_cuda or t.device.index != device:
+    if t.get_device() != device:
         raise ValueError(f"{name} must live on cuda:{device}, got {t.device}")
     if t.dtype != dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
 
 
 class Embedding:
@@ -83,27 +99,23 @@ class Embedding:
             pass
 
     def _ids(self, ids):
+        """(ids, contiguous; their bits)"""
         if not isinstance(ids, torch.Tensor):
             raise TypeError(f"ids: expected a CUDA tensor, got {type(ids)}")
-        if not ids.is_cuda or ids.device.index != self.device:
+        if ids.get_device() != self.device:
             raise ValueError(f"ids must live on cuda:{self.device}, got {ids.device}")
-        if ids.dtype == torch.int32:
-            return ids.contiguous(), 32
-        if ids.dtype == torch.int64:
-            return ids.contiguous(), 64
+        if ids.dtype is torch.int64:
+            return ids if ids.is_contiguous() else ids.contiguous(), 64
+        if ids.dtype is torch.int32:
+            return ids if ids.is_contiguous() else ids.contiguous(), 32
         raise ValueError(f"ids: expected int32 or int64, got {ids.dtype}")
 
     def _rows(self, name, t, shape, dtype):
-        """(tensor, pointer, row stride) of a tensor of rows [C]; the row stride
-        is None when the rows are not evenly spaced runs of C elements."""
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name}: expected a CUDA tensor, got {type(t)}")
-        if not t.is_cuda or t.device.index != self.device:
-            raise ValueError(f"{name} must live on cuda:{self.device}, got {t.device}")
-        if t.dtype != dtype:
-            raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+        """(address, row stride) of a tensor of rows [C]; the row stride is
+        None when the rows are not evenly spaced runs of C elements."""
+        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == self.device and
+                t.shape == shape):
+            _refuse(name, t, shape, dtype, self.device)
         if t.is_contiguous():
             return t.data_ptr(), self.C
         if t.dim() == 2 and (t.stride(1) == 1 or self.C == 1):
@@ -119,7 +131,7 @@ class Embedding:
             ids, bits = self._ids(ids)
             shape = ids.shape + (self.C,)
             if out is None:
-                out = torch.empty(shape, dtype=self.out_dtype, device=ids.device)
+                out = table.new_empty(shape, dtype=self.out_dtype)
                 op, os = out.data_ptr(), self.C
             else:
                 op, os = self._rows("out", out, shape, self.out_dtype)
@@ -288,46 +300,51 @@ class _BlockNormFn(torch.autograd.Function):
 
 
 def _tensor_list(grads, out):
-    """(tensors, the packed eqconv_tensor_t array, its length)."""
+    """(packed array of eqconv_tensor_t, its length, the device's index)"""
     if isinstance(grads, torch.Tensor):
         raise TypeError("expected a list of tensors")
     grads = list(grads)
     outs = grads if out is None else list(out)
     if len(outs) != len(grads):
         raise ValueError(f"out: expected {len(grads)} tensors, got {len(outs)}")
-    dev = None
-    flat = []
-    for i, (g, o) in enumerate(zip(grads, outs)):
-        for t in (g,) if o is g else (g, o):
+    every = grads if out is None else grads + outs
+    if not set(map(type, every)) <= _KINDS:
+        for i, t in enumerate(every):
             if not isinstance(t, torch.Tensor):
-                raise TypeError(f"tensor {i}: expected a CUDA tensor, got {type(t)}")
-            if not t.is_cuda or t.layout != torch.strided:
-                raise ValueError(f"tensor {i}: expected a dense CUDA tensor")
-            if dev is None:
-                dev = t.device
-            if t.device != dev:
-                raise ValueError(f"tensor {i}: lives on {t.device}, the first on {dev}")
-            if not t.is_contiguous() and not torch.ops.aten.is_non_overlapping_and_dense(t):
+                raise TypeError(f"tensor {i % len(grads)}: expected a CUDA tensor, got {type(t)}")
+    places = set(map(torch.Tensor.get_device, every))
+    dev = places.pop() if places else torch.cuda.current_device()
+    if places or dev < 0:
+        raise ValueError("expected CUDA tensors of one device, got " + ", ".join(sorted({str(t.device) for t in every})))
+    kinds, sizes = [g.dtype for g in grads], list(map(torch.Tensor.numel, grads))
+    types = list(map(_TYPES.get, kinds))
+    if None in types:
+        raise ValueError(f"tensor {types.index(None)}: expected torch.float32, bfloat16 or float16, got "
+                         f"{kinds[types.index(None)]}")
+    if out is not None and (kinds != [o.dtype for o in outs] or sizes != list(map(torch.Tensor.numel, outs))):
+        raise ValueError("out: expected the types and sizes of the inputs")
+    if not all(map(torch.Tensor.is_contiguous, every)):
+        for i, (g, o) in enumerate(zip(grads, outs)):
+            if not torch.ops.aten.is_non_overlapping_and_dense(g):
                 raise ValueError(f"tensor {i}: its elements must fill its memory without gaps or repeats")
-        if g.dtype not in _TYPES:
-            raise ValueError(f"tensor {i}: expected torch.float32, bfloat16 or float16, got {g.dtype}")
-        if o is not g and (o.dtype != g.dtype or o.shape != g.shape or o.stride() != g.stride()):
-            raise ValueError(f"out {i}: expected the type, shape and strides of its input")
-        flat += (g.data_ptr(), o.data_ptr(), g.numel(), _TYPES[g.dtype])
-    arr = (B.ctypes.c_int64 * max(1, len(flat)))(*flat)      # four 64-bit words are one eqconv_tensor_t
-    return arr, len(grads), dev
+            if g.shape != o.shape or g.stride() != o.stride():
+                raise ValueError(f"out {i}: expected the shape and strides of its input")
+    at = list(map(torch.Tensor.data_ptr, grads))
+    to = at if out is None else list(map(torch.Tensor.data_ptr, outs))
+    # four 64-bit words are one eqconv_tensor_t
+    return array.array("q", itertools.chain.from_iterable(zip(at, to, sizes, types))), len(grads), dev
 
 
 def gradient_norm(grads, stream=None):
     """sqrt of the sum of all elements' squares, over a list of tensors: a
     0-dimensional fp32 tensor on their device."""
     arr, n, dev = _tensor_list(grads, None)
-    dev = torch.device("cuda", torch.cuda.current_device()) if dev is None else dev
-    with _on(dev.index, stream):
-        norm = torch.empty((), dtype=torch.float32, device=dev)
-        nbytes = B.eqconv_clip_workspace_bytes(n, arr)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        B.eqconv_gradient_norm(n, arr, norm, ws, nbytes)
+    with _on(dev, stream):
+        rows = arr.buffer_info()[0]
+        nbytes = B.eqconv_clip_workspace_bytes(n, rows)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=_device(dev))
+        norm = ws.new_empty((), dtype=torch.float32)
+        B.eqconv_gradient_norm(n, rows, norm, ws, nbytes)
     return norm
 
 
@@ -337,10 +354,10 @@ def clip_gradients(grads, max_norm: float, out=None, eps: float = 1e-6, stream=N
     them), and returns norm (a 0-dimensional fp32 tensor).  A tensor may not
     be in the list twice, nor share memory with another."""
     arr, n, dev = _tensor_list(grads, out)
-    dev = torch.device("cuda", torch.cuda.current_device()) if dev is None else dev
-    with _on(dev.index, stream):
-        norm = torch.empty((), dtype=torch.float32, device=dev)
-        nbytes = B.eqconv_clip_workspace_bytes(n, arr)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        B.eqconv_clip_gradients(n, arr, max_norm, eps, norm, ws, nbytes)
+    with _on(dev, stream):
+        rows = arr.buffer_info()[0]
+        nbytes = B.eqconv_clip_workspace_bytes(n, rows)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=_device(dev))
+        norm = ws.new_empty((), dtype=torch.float32)
+        B.eqconv_clip_gradients(n, rows, max_norm, eps, norm, ws, nbytes)
     return norm
