@@ -21,7 +21,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kChunkBytes = 32768;        // of a tensor, from 16-byte boundary to boundary
-constexpr int kMaxBlocks = 148 * 8;
+// CTAs an SM holds of each kernel at once: the chunks are dealt out to as many, in one wave.
+constexpr int kNormPerSm = 6, kScalePerSm = 5;
+constexpr int kMaxBlocks = 148 * kNormPerSm;
 
 // The tensors of one launch, by value in the kernel's parameters.
 template <int MAXT>
@@ -59,8 +61,9 @@ __device__ __forceinline__ double block_sum(double v, double* red) {
 }
 
 // Calls f(pack, first element, elements valid from, to) for this thread's
-// 16-byte vectors of the chunk; vectors that reach over an end of the tensor
-// are filled element by element (zeros outside).
+// 16-byte vectors of the chunk.  A chunk inside the tensor has all its loads in
+// flight together; in one at an end, vectors that reach over it are filled
+// element by element (zeros outside).
 template <class T, class F>
 __device__ __forceinline__ void over_chunk(const void* base, int64_t n, int chunk, F&& f) {
     constexpr int VE = 16 / sizeof(T);
@@ -69,36 +72,60 @@ __device__ __forceinline__ void over_chunk(const void* base, int64_t n, int chun
     const int off = (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
     const T* origin = p - off;                 // 16-byte boundary at or before p
     const int64_t v0 = (int64_t)chunk * kVecs;
+    if (v0 * VE >= off && (v0 + kVecs) * VE <= n + off) {
+        Pack<T, VE> k[kVecs / kThreads];
+#pragma unroll
+        for (int j = 0; j < kVecs / kThreads; ++j) k[j].load_rw(origin + (v0 + threadIdx.x + j * kThreads) * VE);
+#pragma unroll
+        for (int j = 0; j < kVecs / kThreads; ++j) f(k[j], (v0 + threadIdx.x + j * kThreads) * VE - off, 0, VE);
+        return;
+    }
     const int64_t vecs = (n + off + VE - 1) / VE;
-#pragma unroll 4
     for (int j = threadIdx.x; j < kVecs; j += kThreads) {
         const int64_t v = v0 + j;
         if (v >= vecs) break;
         const int64_t e0 = v * VE - off;       // first element of the vector
         Pack<T, VE> k;
-        if (e0 >= 0 && e0 + VE <= n) {
-            k.load_rw(origin + v * VE);
-            f(k, e0, 0, VE);
-        } else {
-            const int from = e0 < 0 ? (int)-e0 : 0, to = n - e0 < VE ? (int)(n - e0) : VE;
+        const int from = e0 < 0 ? (int)-e0 : 0, to = n - e0 < VE ? (int)(n - e0) : VE;
 #pragma unroll
-            for (int e = 0; e < VE; ++e) k.set(e, e >= from && e < to ? to_float(p[e0 + e]) : 0.f);
-            f(k, e0, from, to);
-        }
+        for (int e = 0; e < VE; ++e) k.set(e, e >= from && e < to ? to_float(p[e0 + e]) : 0.f);
+        f(k, e0, from, to);
     }
 }
 
+// The sum of squares of this thread's elements of a chunk.  fp32 elements go
+// to fp64 one by one.  Of 16-bit ones, two squares are added in fp32 first (the
+// squares have 22 bits at most, so that x^2 + y^2 is rounded once), which halves
+// the conversions to fp64; where such sums may have left the range of fp32,
+// above 2^100 or below 2^-80, the thread adds its elements again in fp64.
 template <class T>
 __device__ __forceinline__ double chunk_squares(const void* base, int64_t n, int chunk) {
-    double s = 0.0;
-    over_chunk<T>(base, n, chunk, [&](const Pack<T, 16 / sizeof(T)>& k, int64_t, int, int) {
+    constexpr int VE = 16 / sizeof(T);
+    const auto wide = [&] {
+        double s[4] = {};        // four sums: an addition in fp64 waits for the last of its own only
+        over_chunk<T>(base, n, chunk, [&](const Pack<T, VE>& k, int64_t, int, int) {
 #pragma unroll
-        for (int e = 0; e < 16 / (int)sizeof(T); ++e) {
-            const double v = (double)k.get(e);
-            s += v * v;
-        }
-    });
-    return s;
+            for (int e = 0; e < VE; ++e) {
+                const double v = (double)k.get(e);
+                s[e & 3] += v * v;
+            }
+        });
+        return (s[0] + s[1]) + (s[2] + s[3]);
+    };
+    if constexpr (sizeof(T) == 4) {
+        return wide();
+    } else {
+        double s[4] = {};
+        over_chunk<T>(base, n, chunk, [&](const Pack<T, VE>& k, int64_t, int, int) {
+#pragma unroll
+            for (int e = 0; e < VE / 2; ++e) {
+                const float x = k.get(2 * e), y = k.get(2 * e + 1);
+                s[e & 3] += (double)fmaf(x, x, y * y);
+            }
+        });
+        const double v = (s[0] + s[1]) + (s[2] + s[3]);
+        return v >= 0x1p-80 && v <= 0x1p100 ? v : wide();
+    }
 }
 
 template <class T>
@@ -122,7 +149,7 @@ __device__ __forceinline__ void scale_chunk(const void* base, void* out_, int64_
 
 // part[first + block] = sum of squares of the block's chunks.
 template <int MAXT>
-__global__ void __launch_bounds__(kThreads) clip_norm_kernel(const __grid_constant__ Table<MAXT> t, double* part) {
+__global__ void __launch_bounds__(kThreads, kNormPerSm) clip_norm_kernel(const __grid_constant__ Table<MAXT> t, double* part) {
     __shared__ double red[kThreads / 32];
     double s = 0.0;
     for (int chunk = blockIdx.x; chunk < t.chunk0[t.count]; chunk += gridDim.x) {
@@ -148,7 +175,7 @@ __global__ void __launch_bounds__(kThreads) clip_total_kernel(const double* part
 }
 
 template <int MAXT>
-__global__ void __launch_bounds__(kThreads) clip_scale_kernel(const __grid_constant__ Table<MAXT> t,
+__global__ void __launch_bounds__(kThreads, kScalePerSm) clip_scale_kernel(const __grid_constant__ Table<MAXT> t,
                                                               const double* part, int parts, float max_norm,
                                                               float eps, float* norm) {
     __shared__ double red[kThreads / 32];
@@ -174,7 +201,7 @@ int64_t chunks_of(const eqconv_tensor_t& t) {
     return t.n > 0 ? (bytes + kChunkBytes - 1) / kChunkBytes : 0;
 }
 
-inline int blocks_for(int64_t chunks) { return (int)(chunks < kMaxBlocks ? chunks : kMaxBlocks); }
+inline int blocks_for(int64_t chunks, int per_sm) { return (int)(chunks < 148 * per_sm ? chunks : 148 * per_sm); }
 
 // Tensors [from, to) of one launch: at most MAXT, and 2^30 chunks.
 template <int MAXT>
@@ -208,7 +235,7 @@ cudaError_t run(int n, const eqconv_tensor_t* ts, bool scale, float max_norm, fl
     for (int from = 0; from < n;) {
         from = fill(t, n, ts, from);
         if (t.count == 0) continue;
-        const int blocks = blocks_for(t.chunk0[t.count]);
+        const int blocks = blocks_for(t.chunk0[t.count], kNormPerSm);
         clip_norm_kernel<MAXT><<<blocks, kThreads, 0, st>>>(t, part + parts);
         count_launch();
         parts += blocks;
@@ -224,8 +251,8 @@ cudaError_t run(int n, const eqconv_tensor_t* ts, bool scale, float max_norm, fl
         if (tables > 1) from = fill(t, n, ts, from);
         else from = n;
         if (t.count == 0) continue;
-        clip_scale_kernel<MAXT><<<blocks_for(t.chunk0[t.count]), kThreads, 0, st>>>(t, part, parts, max_norm, eps,
-                                                                                   first ? norm : nullptr);
+        clip_scale_kernel<MAXT><<<blocks_for(t.chunk0[t.count], kScalePerSm), kThreads, 0, st>>>(
+            t, part, parts, max_norm, eps, first ? norm : nullptr);
         count_launch();
         first = false;
     }

@@ -514,7 +514,8 @@ def test_clip(case, bound):
     outs = [torch.empty_like(t) for t in ts]
     n = layers.clip_gradients(ts, bound, out=outs)
     assert n.dtype == torch.float32 and n.dim() == 0
-    # fp64 sums, one rounding to fp32 of the norm, of k and of the product, one to the type
+    # fp64 sums (of 16-bit elements, of pairs of squares added in fp32: 2^-24 of the sum, half of it in the root), one
+    # rounding to fp32 of the norm, of k and of the product, one to the type
     assert abs(n.item() - want_n) <= 2 * U * want_n
     assert torch.equal(n, layers.gradient_norm(ts))
     for t, b, o, w in zip(ts, before, outs, want):
@@ -534,6 +535,11 @@ def test_clip_range_of_values():
             assert n == float("inf")
         else:
             assert abs(n - want) <= max(2 * U * want, 1.5e-45)
+    for v in (1e-30, 1e-19, 1e19, 3e38):
+        t = torch.full((100000,), v, device="cuda", dtype=torch.bfloat16)
+        t[::7] *= 0.5
+        n, want = layers.gradient_norm([t]).item(), float(np.sqrt((np64(t) ** 2).sum()))
+        assert n == float("inf") if want > 3.4e38 else abs(n - want) <= 2 * U * want
     big = torch.full((1000,), 1e30, device="cuda")
     layers.clip_gradients([big], 1.0)
     assert abs(layers.gradient_norm([big]).item() - 1.0) < 1e-6
