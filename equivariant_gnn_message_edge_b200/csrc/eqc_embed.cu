@@ -260,10 +260,10 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const void* id
     }
 }
 
-// Sort of more nodes: per pass a histogram of every tile of 4096 nodes, a scan
+// Sort of more nodes: per pass a histogram of every tile of 2048 nodes, a scan
 // over the tiles by digit, and a stable scatter.
 constexpr int kLsdThreads = 512;
-constexpr int kLsdRounds = 8;
+constexpr int kLsdRounds = 4;
 constexpr int kLsdTile = kLsdThreads * kLsdRounds;
 static_assert(kLsdThreads == kRadix && kSortThreads == 2 * kRadix, "one and two threads per digit");
 
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kLsdThreads) embed_scatter_kernel(const void* 
 // Rows of a block that writes zeros: 512 KB of them, so that the search takes
 // little of its time, and at most 2048.
 constexpr int kZeroRows = 2048, kZeroBytes = 512 * 1024;
-constexpr int64_t kSortZeroBytes = 96 << 20;
+constexpr int64_t kSortZeroBytes = 64 << 20;
 
 struct SumParams {
     const int *keys, *perm;   // nodes in type order
@@ -431,23 +431,34 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const SumParams p, const
         for (int e = 0; e < VE; ++e) out.e[e] = acc[e];
         out.store(part + which * p.C);
     };
+    // batches of 8 rows in flight; the next batch's keys and places are fetched while they are
     constexpr int kAhead = 8;
-    for (int j0 = 0; j0 < n; j0 += kAhead) {
-        Pack<O, VE> in[kAhead];
-        int key[kAhead];
+    int key[kAhead], at[kAhead];
+    const auto fetch = [&](int j0) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             key[u] = j0 + u < n ? __ldg(keys + j0 + u) : none;
-            if (key[u] != none) in[u].load(gy + (int64_t)__ldg(perm + j0 + u) * p.ldg + c);
+            at[u] = j0 + u < n ? __ldg(perm + j0 + u) : 0;
         }
+    };
+    fetch(0);
+    for (int j0 = 0; j0 < n; j0 += kAhead) {
+        Pack<O, VE> in[kAhead];
+        int now[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            now[u] = key[u];
+            if (key[u] != none) in[u].load(gy + (int64_t)at[u] * p.ldg + c);
+        }
+        fetch(j0 + kAhead);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             if (j0 + u >= n) break;
-            if (key[u] != cur) {
+            if (now[u] != cur) {
                 if (begun_before) partial(0);
                 else row(cur);
                 begun_before = false;
-                cur = key[u];
+                cur = now[u];
 #pragma unroll
                 for (int e = 0; e < VE; ++e) acc[e] = 0.f;
             }
@@ -567,8 +578,8 @@ cudaError_t embed_forward(const EmbedArgs& a, const void* table, int64_t table_s
 namespace {
 
 // How the sum is cut for (N, C): slabs of 32 vectors (or one slab of fewer
-// lanes), and tiles of R nodes so that about 32 workers run on every SM, with
-// whole batches of 8 rows in flight.
+// lanes), and tiles of R nodes so that about 16 warps run on every SM (as many
+// as their registers allow), with whole batches of 8 rows in flight.
 struct SumShape {
     int ve, lx_log2, slabs, R, tiles;
 };
@@ -579,7 +590,7 @@ SumShape sum_shape(int64_t N, int C, int ve) {
     while (s.lx_log2 < 5 && (1 << s.lx_log2) < vecs) ++s.lx_log2;
     s.slabs = cdiv(vecs, 1 << s.lx_log2);
     const int64_t lanes = N * s.slabs << s.lx_log2;
-    int64_t R = (lanes / (148 * 1024) + 7) / 8 * 8;
+    int64_t R = (lanes / (148 * 512) + 7) / 8 * 8;
     s.R = (int)(R < 8 ? 8 : R > 256 ? 256 : R);
     s.tiles = cdiv(N, s.R);
     return s;
@@ -712,7 +723,7 @@ cudaError_t embed_backward(const EmbedArgs& a, const void* gy, int64_t gy_stride
     const int bits = bit_length(a.V), passes = cdiv(bits, kDigitBits), digit_bits = cdiv(bits, passes);
     cudaError_t err;
     // A sort of one cluster leaves the other SMs idle for some 10 us: they write zeros to the first rows meanwhile
-    // (whole 16 bytes, up to 96 MB), and the sums overwrite those that have nodes.
+    // (whole 16 bytes, up to 64 MB), and the sums overwrite those that have nodes.
     int64_t zero_to = 0;
     const int64_t row = (int64_t)a.C * type_bytes(a.in_type);
     if (a.N <= (int64_t)kMaxCluster * kSortCap) {
