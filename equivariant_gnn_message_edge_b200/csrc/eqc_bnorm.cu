@@ -82,9 +82,9 @@ Staged staged_for_args(const BlockNormArgs& a, bool bwd) {
                           (const void*)a.dx, (const void*)a.db, (const void*)a.dgate, (const void*)a.w_post,
                           (const void*)a.w_pre})
         all |= reinterpret_cast<uintptr_t>(q);
-    if (all % 16 != 0) return Staged{};
     const int tensors = bwd ? 2 * (a.g_h != nullptr) + (a.b != nullptr) + (a.g_x != nullptr) : 1 + (a.b != nullptr);
-    return tensors ? staged_shape(a.L, a.C, type_bytes(a.type), tensors, a.gate != nullptr, bwd) : Staged{};
+    if (!tensors) return Staged{};
+    return staged_shape(a.L, a.C, type_bytes(a.type), tensors, a.gate != nullptr, bwd, all % 16 == 0);
 }
 
 // rows: of the partial sums a CTA leaves (see bn_dw_reduce).
@@ -92,30 +92,28 @@ cudaError_t run(BnParams& p, const BlockNormArgs& a, bool bwd, cudaStream_t st, 
     const Staged h = staged_for_args(a, bwd);
     if (h.slots) {
         StagedParams s{};
-        const int es = type_bytes(a.type);
+        const int es = type_bytes(a.type), node = (a.L + 1) * (a.L + 1) * a.C * es, gate = (a.L + 1) * a.C * es;
         p.width = h.width;
         s.slots = h.slots;
         s.nodes = h.nodes;
+        s.ring = h.ring;
         s.total = ((int64_t)a.N + h.nodes - 1) / h.nodes;
-        s.node_bytes = (a.L + 1) * (a.L + 1) * a.C * es;
-        s.gate_bytes = a.gate ? (a.L + 1) * a.C * es : 0;
         int o = 0;
         const auto place = [&](bool there, const void* from, int bytes) {
-            const int at = o;
-            if (there) {
-                s.from[s.tensors] = static_cast<const unsigned char*>(from);
-                s.bytes[s.tensors] = bytes;
-                s.offset[s.tensors++] = at;
-                o += bytes * h.nodes;
-            }
-            return at;
+            if (!there) return 0;
+            s.from[s.tensors] = static_cast<const unsigned char*>(from);
+            s.bytes[s.tensors] = bytes;
+            s.offset[s.tensors] = o;
+            o += (int)part_bytes((int64_t)bytes * h.nodes, h.apart);
+            return s.tensors++;
         };
-        s.o_x = place(!bwd || a.g_h, a.x, s.node_bytes);
-        s.o_b = place(a.b, a.b, s.node_bytes);
-        s.o_gx = place(bwd && a.g_x, a.g_x, s.node_bytes);
-        s.o_gh = place(bwd && a.g_h, a.g_h, s.node_bytes);
-        s.o_g = place(a.gate, a.gate, s.gate_bytes);
+        s.i_x = place(!bwd || a.g_h, a.x, node);
+        s.i_b = place(a.b, a.b, node);
+        s.i_gx = place(bwd && a.g_x, a.g_x, node);
+        s.i_gh = place(bwd && a.g_h, a.g_h, node);
+        s.i_g = place(a.gate, a.gate, gate);
         s.slot_bytes = o;
+        s.ends = 16 / (gate * h.nodes) + 2;
         s.status = a.status;
         const int64_t most = (int64_t)kSMs * h.ctas;
         const int grid = (int)(s.total < most ? s.total : most);

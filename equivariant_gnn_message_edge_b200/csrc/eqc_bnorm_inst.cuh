@@ -28,7 +28,9 @@ cudaError_t EQC_BN_NAME(BnParams& p, const Shape& s, bool bwd, cudaStream_t st) 
 }
 
 cudaError_t EQC_BN_STAGED(const StagedParams& s, const Staged& h, int grid, bool bwd, cudaStream_t st) {
-    return bwd ? staged_for<EQC_BN_TYPE, true>(s, h, grid, st) : staged_for<EQC_BN_TYPE, false>(s, h, grid, st);
+    using T = EQC_BN_TYPE;
+    if (h.apart) return bwd ? staged_for<T, true, true>(s, h, grid, st) : staged_for<T, false, true>(s, h, grid, st);
+    return bwd ? staged_for<T, true, false>(s, h, grid, st) : staged_for<T, false, false>(s, h, grid, st);
 }
 
 }  // namespace bn

@@ -3,12 +3,15 @@
 // degrees are contiguous in every tensor, so a slot is one copy per tensor; the
 // copies of the next slots run while the current ones are summed and written,
 // which is what the register-resident kernels of eqc_bnorm.cuh lack (their
-// loads, sums and stores follow one another in each warp).  Used where the
-// tensors are 16-byte aligned, C is whole 16-byte vectors and two slots fit.
+// loads, sums and stores follow one another in each warp).  Used where two
+// slots fit.  Rows that are no whole 16 bytes, or start off that boundary, are
+// copied with the bytes around them up to the boundary (they are other nodes'),
+// and a thread's channels are then `width` apart instead of neighbours, so that
+// every element is read alone and a warp's lanes still lie side by side.
 //
 // A worker is a warp (32 / width nodes a slot, each warp with slots of its own)
 // or, for wide nodes, the whole CTA (one node a slot).  Its threads own V
-// neighbouring channels of every row of the node.
+// channels of every row of the node.
 #pragma once
 
 #include "eqc_bnorm.cuh"
@@ -27,7 +30,9 @@ struct StagedParams {
     int tensors;
     const unsigned char* from[5];
     int bytes[5], offset[5];
-    int o_x, o_b, o_gx, o_gh, o_g, slot_bytes, node_bytes, gate_bytes;
+    int i_x, i_b, i_gx, i_gh, i_g;       // which of them is which
+    int slot_bytes, ring;      // bytes of a slot; where the ring begins in shared memory
+    int ends;                  // the first and last slots whose pieces may reach over a tensor's ends
     unsigned* status;
 };
 
@@ -36,28 +41,104 @@ struct Ring {
     uint64_t* full;            // a phase: one arrival per tensor, and its bytes
 };
 
+// The 16-byte pieces that hold tensor t of the nodes of one slot.
+struct Window {
+    const unsigned char* at;   // the first piece
+    uint32_t lead, bytes;      // the nodes begin `lead` bytes into it; all bytes are there
+    bool inside;               // every piece lies in the tensor
+};
+__device__ __forceinline__ Window window(const StagedParams& s, int t, int64_t g) {
+    const int64_t n0 = g * s.nodes, left = s.p.N - n0, nodes = left < s.nodes ? left : s.nodes;
+    const unsigned char* p = s.from[t] + n0 * s.bytes[t];
+    Window w;
+    w.lead = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
+    w.at = p - w.lead;
+    w.bytes = (w.lead + (uint32_t)(nodes * s.bytes[t]) + 15) & ~15u;
+    w.inside = w.at >= s.from[t] && w.at + w.bytes <= s.from[t] + (int64_t)s.p.N * s.bytes[t];
+    return w;
+}
+
 // Copies of sequence number k of this CTA into its slot: tensor t by lane t,
 // so that the warp that does it is held up by one copy's instructions only.
 __device__ __forceinline__ void fill(const StagedParams& s, const Ring& r, int k, int lane) {
     const int64_t g = blockIdx.x + (int64_t)k * gridDim.x;
     if (g >= s.total || lane >= s.tensors) return;
-    const int64_t n0 = g * s.nodes;
-    const uint32_t nodes = (uint32_t)(s.p.N - n0 < s.nodes ? s.p.N - n0 : s.nodes), bytes = nodes * s.bytes[lane];
+    const Window w = window(s, lane, g);
     const int slot = k % s.slots;
-    bulk::expect(r.full + slot, bytes);
-    bulk::copy(r.base + (int64_t)slot * s.slot_bytes + s.offset[lane], s.from[lane] + n0 * s.bytes[lane], bytes,
-               r.full + slot);
+    bulk::expect(r.full + slot, w.inside ? w.bytes : 0);
+    if (w.inside) bulk::copy(r.base + (int64_t)slot * s.slot_bytes + s.offset[lane], w.at, w.bytes, r.full + slot);
 }
 
-// What one thread sees of its node: the tensors' slot parts at its channels.
+// How far into its first piece the nodes of a slot begin.
+__device__ __forceinline__ uint32_t lead_of(const StagedParams& s, int t, int64_t g) {
+    return ((uint32_t)reinterpret_cast<uintptr_t>(s.from[t]) + (uint32_t)g * s.nodes * s.bytes[t]) & 15u;
+}
+
+// The first and last nodes' pieces that reach over the tensor's ends are
+// copied element by element, by the threads that wait for the slot (`lane` of
+// `lanes`).  True if there were any: the caller then waits for the others.
+template <class T>
+__device__ __forceinline__ bool fill_ends(const StagedParams& s, const Ring& r, int k, int lane, int lanes) {
+    const int64_t g = blockIdx.x + (int64_t)k * gridDim.x;
+    if (g >= s.ends && g + s.ends < s.total) return false;
+    bool any = false;
+    for (int t = 0; t < s.tensors; ++t) {
+        const Window w = window(s, t, g);
+        if (w.inside) continue;
+        any = true;
+        const int64_t n0 = g * s.nodes, left = s.p.N - n0, nodes = left < s.nodes ? left : s.nodes;
+        const T* from = reinterpret_cast<const T*>(w.at + w.lead);
+        T* to = reinterpret_cast<T*>(r.base + (int64_t)(k % s.slots) * s.slot_bytes + s.offset[t] + w.lead);
+        for (int i = lane; i < (int)(nodes * s.bytes[t] / sizeof(T)); i += lanes) to[i] = from[i];
+    }
+    if (any) bulk::fence_writes();       // the slot's next copies come behind these
+    return any;
+}
+
+// A thread's V channels of a row: neighbours from `first` (on the vector's
+// boundary), or (APART) first, first + step, ... below C, zeros behind C.
+template <int V, bool APART>
+struct Lanes {
+    int first, step, C;
+    template <class T>
+    __device__ __forceinline__ void load(F2 (&v)[V / 2], const T* row) const {
+        if constexpr (!APART) {
+            load2<T, V>(v, row + first);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                const int c = first + 2 * i * step, d = c + step;
+                v[i] = F2(c < C ? to_float(row[c]) : 0.f, d < C ? to_float(row[d]) : 0.f);
+            }
+        }
+    }
+    template <class T>
+    __device__ __forceinline__ void store(T* row, const F2 (&v)[V / 2]) const {
+        if constexpr (!APART) {
+            store2<T, V>(row + first, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                const int c = first + 2 * i * step, d = c + step;
+                float x, y;
+                v[i].split(x, y);
+                if (c < C) row[c] = from_float<T>(x);
+                if (d < C) row[d] = from_float<T>(y);
+            }
+        }
+    }
+};
+
+// What one worker sees of its node: the tensors' slot parts.
 template <class T>
 struct View {
     const T *x, *b, *gx, *gh, *g;
 };
 
-template <class T, int V, int L>
-__device__ __forceinline__ void fwd_node(const BnParams& p, const View<T>& s, const float* w, bool own, bool live,
-                                         int64_t row, int64_t srow, int c0, bool lead, WorkerSum<L + 1>& sum) {
+template <class T, int V, int L, bool APART>
+__device__ __forceinline__ void fwd_node(const BnParams& p, const View<T>& s, const float* w, const Lanes<V, APART>& q,
+                                         bool own, bool live, int64_t row, int64_t srow, bool lead,
+                                         WorkerSum<L + 1>& sum) {
     constexpr int H = V / 2;
     const bool post = p.b != nullptr, pre = p.w_pre != nullptr, gated = p.gate != nullptr;
     float sb[L + 1], sy[L + 1];
@@ -71,7 +152,7 @@ __device__ __forceinline__ void fwd_node(const BnParams& p, const View<T>& s, co
 #pragma unroll
                 for (int m = 0; m < 2 * l + 1; ++m) {
                     F2 b[H];
-                    load2<T, V>(b, s.b + (l * l + m) * p.C);
+                    q.load(b, s.b + (l * l + m) * p.C);
 #pragma unroll
                     for (int i = 0; i < H; ++i) v = fma2(b[i], b[i], v);
                 }
@@ -85,12 +166,12 @@ __device__ __forceinline__ void fwd_node(const BnParams& p, const View<T>& s, co
         if (post) sb[l] = rsqrtf(sb[l] * (1.f / ((2 * l + 1) * (float)p.C)) + p.eps);
         if (!own) continue;
         if (post) {
-            load2<float, V>(k[l], w + l * p.C + c0);
+            q.load(k[l], w + l * p.C);
 #pragma unroll
             for (int i = 0; i < H; ++i) k[l][i] = mul2(k[l][i], F2(p.scale * sb[l]));
             if (gated) {
                 F2 g[H], a[H], da[H];
-                load2<T, V>(g, s.g + l * p.C);
+                q.load(g, s.g + l * p.C);
                 gate_values<V, sizeof(T) == 2>(p.gate_kind, g, a, da);
 #pragma unroll
                 for (int i = 0; i < H; ++i) k[l][i] = mul2(k[l][i], a[i]);
@@ -100,13 +181,13 @@ __device__ __forceinline__ void fwd_node(const BnParams& p, const View<T>& s, co
 #pragma unroll
         for (int m = 0; m < 2 * l + 1; ++m) {
             F2 y[H];
-            load2<T, V>(y, s.x + (l * l + m) * p.C);
+            q.load(y, s.x + (l * l + m) * p.C);
             if (post) {
                 F2 b[H];
-                load2<T, V>(b, s.b + (l * l + m) * p.C);
+                q.load(b, s.b + (l * l + m) * p.C);
 #pragma unroll
                 for (int i = 0; i < H; ++i) y[i] = fma2(k[l][i], b[i], y[i]);
-                if (live) store2<T, V>(static_cast<T*>(p.x_out) + row + (l * l + m) * p.C + c0, y);
+                if (live) q.store(static_cast<T*>(p.x_out) + row + (l * l + m) * p.C, y);
             }
 #pragma unroll
             for (int i = 0; i < H; ++i) v = fma2(y[i], y[i], v);
@@ -120,22 +201,22 @@ __device__ __forceinline__ void fwd_node(const BnParams& p, const View<T>& s, co
             sy[l] = rsqrtf(sy[l] * (1.f / ((2 * l + 1) * (float)p.C)) + p.eps);
             if (!own) continue;
             F2 wi[H];
-            load2<float, V>(wi, w + (L + 1 + l) * p.C + c0);
+            q.load(wi, w + (L + 1 + l) * p.C);
 #pragma unroll
             for (int i = 0; i < H; ++i) wi[i] = mul2(wi[i], F2(sy[l]));
 #pragma unroll
             for (int m = 0; m < 2 * l + 1; ++m) {
                 F2 y[H];
-                load2<T, V>(y, s.x + (l * l + m) * p.C);
+                q.load(y, s.x + (l * l + m) * p.C);
                 if (post) {
                     F2 b[H];
-                    load2<T, V>(b, s.b + (l * l + m) * p.C);
+                    q.load(b, s.b + (l * l + m) * p.C);
 #pragma unroll
                     for (int i = 0; i < H; ++i) y[i] = fma2(k[l][i], b[i], y[i]);
                 }
 #pragma unroll
                 for (int i = 0; i < H; ++i) y[i] = mul2(y[i], wi[i]);
-                if (live) store2<T, V>(static_cast<T*>(p.h) + row + (l * l + m) * p.C + c0, y);
+                if (live) q.store(static_cast<T*>(p.h) + row + (l * l + m) * p.C, y);
             }
         }
     }
@@ -149,9 +230,9 @@ __device__ __forceinline__ void fwd_node(const BnParams& p, const View<T>& s, co
 
 // kKeep (fp32): t goes into the slot in the place of g_h, so that db needs no
 // second pass over x, g_x and g_h; 16 bits would round it, so it is made again.
-template <class T, int V, int L>
-__device__ __forceinline__ void bwd_node(const BnParams& p, const View<T>& s, const float* w, bool own, bool live,
-                                         int64_t row, int64_t grow, int c0, const float (&sb)[L + 1],
+template <class T, int V, int L, bool APART>
+__device__ __forceinline__ void bwd_node(const BnParams& p, const View<T>& s, const float* w, const Lanes<V, APART>& q,
+                                         bool own, bool live, int64_t row, int64_t grow, const float (&sb)[L + 1],
                                          const float (&sy)[L + 1], F2 (&dwo)[L + 1][V / 2], F2 (&dwi)[L + 1][V / 2],
                                          WorkerSum<L + 1>& sum) {
     constexpr int H = V / 2;
@@ -161,7 +242,7 @@ __device__ __forceinline__ void bwd_node(const BnParams& p, const View<T>& s, co
     float mpy[L + 1], mqb[L + 1];
     // y of a row: x + k b with k = sa sb w_post
     const auto y_of = [&](int r, const F2 (&k)[H], const F2 (&b)[H], F2 (&y)[H]) {
-        load2<T, V>(y, s.x + r * p.C);
+        q.load(y, s.x + r * p.C);
         if (post)
 #pragma unroll
             for (int i = 0; i < H; ++i) y[i] = fma2(k[i], b[i], y[i]);
@@ -172,7 +253,7 @@ __device__ __forceinline__ void bwd_node(const BnParams& p, const View<T>& s, co
         if (!own) continue;
         if (gated) {
             F2 g[H];
-            load2<T, V>(g, s.g + l * p.C);
+            q.load(g, s.g + l * p.C);
             gate_values<V, sizeof(T) == 2>(p.gate_kind, g, sa[l], da[l]);
         }
 #pragma unroll
@@ -182,18 +263,18 @@ __device__ __forceinline__ void bwd_node(const BnParams& p, const View<T>& s, co
         }
         if (!pre) continue;
         F2 wi[H], k[H], b[H], v(0.f);
-        load2<float, V>(wi, w + (L + 1 + l) * p.C + c0);
+        q.load(wi, w + (L + 1 + l) * p.C);
         if (post) {
-            load2<float, V>(k, w + l * p.C + c0);
+            q.load(k, w + l * p.C);
 #pragma unroll
             for (int i = 0; i < H; ++i) k[i] = mul2(mul2(k[i], sa[l][i]), F2(sb[l]));
         }
 #pragma unroll
         for (int m = 0; m < 2 * l + 1; ++m) {
             F2 gh[H], y[H];
-            if (post) load2<T, V>(b, s.b + (l * l + m) * p.C);
+            if (post) q.load(b, s.b + (l * l + m) * p.C);
             y_of(l * l + m, k, b, y);
-            load2<T, V>(gh, s.gh + (l * l + m) * p.C);
+            q.load(gh, s.gh + (l * l + m) * p.C);
 #pragma unroll
             for (int i = 0; i < H; ++i) v = fma2(mul2(gh[i], wi[i]), y[i], v);
         }
@@ -208,8 +289,8 @@ __device__ __forceinline__ void bwd_node(const BnParams& p, const View<T>& s, co
     for (int l = 0; l <= L; ++l) {
         if (!own) continue;
         F2 wi[H], wo[H], k[H], tb[H], gy[H];      // wi: sy w_pre
-        if (pre) load2<float, V>(wi, w + (L + 1 + l) * p.C + c0);
-        if (post) load2<float, V>(wo, w + l * p.C + c0);
+        if (pre) q.load(wi, w + (L + 1 + l) * p.C);
+        if (post) q.load(wo, w + l * p.C);
         const F2 m1(-mpy[l]), s1(sy[l]), s0(sb[l]);
 #pragma unroll
         for (int i = 0; i < H; ++i) {
@@ -221,27 +302,27 @@ __device__ __forceinline__ void bwd_node(const BnParams& p, const View<T>& s, co
         for (int m = 0; m < 2 * l + 1; ++m) {
             const int r = l * l + m;
             F2 t[H], b[H];
-            if (post) load2<T, V>(b, s.b + r * p.C);
-            if (more) load2<T, V>(t, s.gx + r * p.C);
+            if (post) q.load(b, s.b + r * p.C);
+            if (more) q.load(t, s.gx + r * p.C);
             else
 #pragma unroll
                 for (int i = 0; i < H; ++i) t[i] = F2(0.f);
             if (pre) {
                 F2 gh[H], y[H];
                 y_of(r, k, b, y);
-                load2<T, V>(gh, s.gh + r * p.C);
+                q.load(gh, s.gh + r * p.C);
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
                     t[i] = fma2(gh[i], wi[i], fma2(y[i], m1, t[i]));
                     gy[i] = fma2(gh[i], y[i], gy[i]);
                 }
                 if constexpr (kKeep)
-                    if (post) store2<T, V>(const_cast<T*>(s.gh) + r * p.C, t);
+                    if (post) q.store(const_cast<T*>(s.gh) + r * p.C, t);
             }
             if (post)
 #pragma unroll
                 for (int i = 0; i < H; ++i) tb[i] = fma2(t[i], b[i], tb[i]);
-            if (live) store2<T, V>(static_cast<T*>(p.dx) + row + r * p.C + c0, t);
+            if (live) q.store(static_cast<T*>(p.dx) + row + r * p.C, t);
         }
         F2 v(0.f), dg[H];
 #pragma unroll
@@ -255,7 +336,7 @@ __device__ __forceinline__ void bwd_node(const BnParams& p, const View<T>& s, co
             if (live && pre) dwi[l][i] = fma2(gy[i], s1, dwi[l][i]);
         }
         mqb[l] = v.sum();
-        if (gated && live) store2<T, V>(static_cast<T*>(p.dgate) + grow + l * p.C + c0, dg);
+        if (gated && live) q.store(static_cast<T*>(p.dgate) + grow + l * p.C, dg);
     }
     if (!post) return;
     sum(mqb);
@@ -265,11 +346,11 @@ __device__ __forceinline__ void bwd_node(const BnParams& p, const View<T>& s, co
         if (!own) continue;
         F2 wi[H], k[H];
         const F2 m1(-mpy[l]), m2(-mqb[l]);
-        load2<float, V>(k, w + l * p.C + c0);
+        q.load(k, w + l * p.C);
 #pragma unroll
         for (int i = 0; i < H; ++i) k[i] = mul2(mul2(k[i], sa[l][i]), F2(sb[l]));
         if (pre && !kKeep) {
-            load2<float, V>(wi, w + (L + 1 + l) * p.C + c0);
+            q.load(wi, w + (L + 1 + l) * p.C);
 #pragma unroll
             for (int i = 0; i < H; ++i) wi[i] = mul2(wi[i], F2(sy[l]));
         }
@@ -277,31 +358,31 @@ __device__ __forceinline__ void bwd_node(const BnParams& p, const View<T>& s, co
         for (int m = 0; m < 2 * l + 1; ++m) {
             const int r = l * l + m;
             F2 t[H], b[H];
-            load2<T, V>(b, s.b + r * p.C);
+            q.load(b, s.b + r * p.C);
             if (pre && kKeep) {
-                load2<T, V>(t, s.gh + r * p.C);
+                q.load(t, s.gh + r * p.C);
             } else {
-                if (more) load2<T, V>(t, s.gx + r * p.C);
+                if (more) q.load(t, s.gx + r * p.C);
                 else
 #pragma unroll
                     for (int i = 0; i < H; ++i) t[i] = F2(0.f);
                 if (pre) {
                     F2 gh[H], y[H];
                     y_of(r, k, b, y);
-                    load2<T, V>(gh, s.gh + r * p.C);
+                    q.load(gh, s.gh + r * p.C);
 #pragma unroll
                     for (int i = 0; i < H; ++i) t[i] = fma2(gh[i], wi[i], fma2(y[i], m1, t[i]));
                 }
             }
 #pragma unroll
             for (int i = 0; i < H; ++i) t[i] = fma2(k[i], t[i], mul2(b[i], m2));
-            if (live) store2<T, V>(static_cast<T*>(p.db) + row + r * p.C + c0, t);
+            if (live) q.store(static_cast<T*>(p.db) + row + r * p.C, t);
         }
     }
 }
 
 // Shared memory: [w_post, w_pre: 2 (L + 1) C floats] [ring of slots].
-template <class T, int V, int L, bool BWD, bool CTA>
+template <class T, int V, int L, bool BWD, bool CTA, bool APART>
 __global__ void __launch_bounds__(CTA ? 256 : BWD ? 256 : 512, 1) bn_staged_kernel(const StagedParams s) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ uint64_t full[kMaxSlots];
@@ -309,12 +390,12 @@ __global__ void __launch_bounds__(CTA ? 256 : BWD ? 256 : 512, 1) bn_staged_kern
     constexpr int D = (L + 1) * (L + 1);
     const BnParams& p = s.p;
     float* w = reinterpret_cast<float*>(smem);
-    const Ring ring{smem + 2 * (L + 1) * p.C * sizeof(float), full};
+    const Ring ring{smem + s.ring, full};
     const int workers = CTA ? 1 : blockDim.x / 32, worker = CTA ? 0 : threadIdx.x / 32;
     const int lane = CTA ? threadIdx.x : threadIdx.x & 31;
     const int width = CTA ? (int)blockDim.x : p.width;
     const int sub = CTA ? 0 : lane / width, x0 = lane - sub * width;
-    const int c0 = x0 * V;
+    const Lanes<V, APART> q{APART ? x0 : x0 * V, width, p.C};
     if (threadIdx.x == 0) {
         for (int i = 0; i < s.slots; ++i) bulk::init(full + i, s.tensors);
         bulk::fence_init();
@@ -326,7 +407,7 @@ __global__ void __launch_bounds__(CTA ? 256 : BWD ? 256 : 512, 1) bn_staged_kern
     __syncthreads();
     if (threadIdx.x < 32)
         for (int k = 0; k < s.slots; ++k) fill(s, ring, k, threadIdx.x);
-    const bool own = c0 < p.C;
+    const bool own = q.first < p.C;
     F2 dwo[BWD ? L + 1 : 1][V / 2], dwi[BWD ? L + 1 : 1][V / 2];
 #pragma unroll
     for (int l = 0; l < (BWD ? L + 1 : 1); ++l)
@@ -362,17 +443,22 @@ __global__ void __launch_bounds__(CTA ? 256 : BWD ? 256 : 512, 1) bn_staged_kern
             ok = false;
             break;
         }
+        if constexpr (APART)
+            if (fill_ends<T>(s, ring, k, lane, CTA ? blockDim.x : 32)) {
+                if constexpr (CTA) __syncthreads();
+                else __syncwarp();
+            }
         const unsigned char* base = ring.base + (int64_t)slot * s.slot_bytes;
-        const auto at = [&](int o, int bytes) {
-            return reinterpret_cast<const T*>(base + o + sub * bytes) + c0;
+        const auto at = [&](int t) {
+            const uint32_t lead = APART ? lead_of(s, t, blockIdx.x + (int64_t)k * gridDim.x) : 0;
+            return reinterpret_cast<const T*>(base + s.offset[t] + lead + sub * s.bytes[t]);
         };
-        const View<T> v{at(s.o_x, s.node_bytes), at(s.o_b, s.node_bytes), at(s.o_gx, s.node_bytes),
-                        at(s.o_gh, s.node_bytes), at(s.o_g, s.gate_bytes)};
+        const View<T> v{at(s.i_x), at(s.i_b), at(s.i_gx), at(s.i_gh), at(s.i_g)};
         const int64_t row = n * D * p.C, grow = n * (L + 1) * p.C;
         if constexpr (BWD)
-            bwd_node<T, V, L>(p, v, w, own, live, row, grow, c0, sb, sy, dwo, dwi, sum);
+            bwd_node<T, V, L, APART>(p, v, w, q, own, live, row, grow, sb, sy, dwo, dwi, sum);
         else
-            fwd_node<T, V, L>(p, v, w, own, live, row, n * (L + 1), c0, x0 == 0, sum);
+            fwd_node<T, V, L, APART>(p, v, w, q, own, live, row, n * (L + 1), x0 == 0, sum);
         // everyone has read (and written) the slot: its next copies may come
         if constexpr (BWD && sizeof(T) == 4) bulk::fence_writes();
         if constexpr (CTA) __syncthreads();
@@ -391,20 +477,20 @@ __global__ void __launch_bounds__(CTA ? 256 : BWD ? 256 : 512, 1) bn_staged_kern
 #pragma unroll
             for (int l = 0; l <= L; ++l)
                 if (own) {
-                    store2<float, V>(part + l * p.C + c0, dwo[l]);
-                    store2<float, V>(part + (L + 1 + l) * p.C + c0, dwi[l]);
+                    q.store(part + l * p.C, dwo[l]);
+                    q.store(part + (L + 1 + l) * p.C, dwi[l]);
                 }
         } else {
             // the warps' sums in order, and within a warp its nodes', one degree and kind at a time
             __syncthreads();      // every slot has been read
-            float* t = reinterpret_cast<float*>(smem + 2 * (L + 1) * p.C * sizeof(float));
+            float* t = reinterpret_cast<float*>(smem + s.ring);
 #pragma unroll
             for (int l = 0; l <= L; ++l)
 #pragma unroll
                 for (int which = 0; which < 2; ++which) {
-                    store2<float, V>(t + threadIdx.x * V, which ? dwi[l] : dwo[l]);
+                    const int groups = workers * (32 / width), mine_at = (threadIdx.x / width) * width * V;
+                    Lanes<V, APART>{q.first, q.step, width * V}.store(t + mine_at, which ? dwi[l] : dwo[l]);
                     __syncthreads();
-                    const int groups = workers * (32 / width);
                     for (int c = threadIdx.x; c < p.C; c += blockDim.x) {
                         float v = 0.f;
                         for (int g = 0; g < groups; ++g) v += t[(g * width) * V + c];
@@ -443,7 +529,7 @@ struct CtaSum {
     }
 };
 
-template <class T, int V, int J, bool BWD>
+template <class T, int V, int J, bool BWD, bool APART>
 __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(const StagedParams s) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ uint64_t full[kMaxSlots];
@@ -452,7 +538,6 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
     const Ring ring{smem, full};
     const bool post = p.b != nullptr, gated = p.gate != nullptr;
     const bool pre = BWD ? p.g_h != nullptr : p.w_pre != nullptr, more = p.g_x != nullptr;
-    const int c0 = threadIdx.x * V, cstep = blockDim.x * V;
     const float inv_m = 1.f / (float)p.C;
     if (threadIdx.x < 32) red[threadIdx.x] = 0.f;
     if (threadIdx.x == 0) {
@@ -464,12 +549,15 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
         for (int k = 0; k < s.slots; ++k) fill(s, ring, k, threadIdx.x);
     constexpr int H = V / 2;
     bool own[J];
+    Lanes<V, APART> q[J];
     F2 wo[J][H], wi[J][H], dwo[J][H], dwi[J][H];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-        own[j] = c0 + j * cstep < p.C;
-        if (own[j] && post) load2<float, V>(wo[j], p.w_post + c0 + j * cstep);
-        if (own[j] && pre) load2<float, V>(wi[j], p.w_pre + c0 + j * cstep);
+        q[j] = Lanes<V, APART>{(int)(APART ? threadIdx.x + j * V * blockDim.x : (threadIdx.x + j * blockDim.x) * V),
+                               (int)blockDim.x, p.C};
+        own[j] = q[j].first < p.C;
+        if (own[j] && post) q[j].load(wo[j], p.w_post);
+        if (own[j] && pre) q[j].load(wi[j], p.w_pre);
 #pragma unroll
         for (int i = 0; i < H; ++i) dwo[j][i] = dwi[j][i] = F2(0.f);
     }
@@ -494,10 +582,15 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
                 for (int i = 0; i < s.slots; ++i) bulk::wait(full + i, 0), bulk::wait(full + i, 1);
             return;
         }
+        if constexpr (APART)
+            if (fill_ends<T>(s, ring, k, threadIdx.x, blockDim.x)) __syncthreads();
         const unsigned char* base = ring.base + (int64_t)slot * s.slot_bytes;
-        const auto at = [&](int o, int j) { return reinterpret_cast<const T*>(base + o) + c0 + j * cstep; };
-        const auto to = [&](void* q, int j) { return static_cast<T*>(q) + n * p.C + c0 + j * cstep; };
-        const auto release = [&] {       // behind a barrier: every thread has read the slot
+        const auto at = [&](int t) {
+            const uint32_t lead = APART ? lead_of(s, t, n) : 0;
+            return reinterpret_cast<const T*>(base + s.offset[t] + lead);
+        };
+        const auto to = [&](void* y) { return static_cast<T*>(y) + n * p.C; };
+        const auto release = [&] {       // behind a barrier: every thread has read the slot (and written its ends)
             if (threadIdx.x < 32) fill(s, ring, k + s.slots, threadIdx.x);
         };
         // y: x, then x_out; bs: b, then b / rms(b); sa, da: scale a(gate), scale a'(gate)
@@ -505,11 +598,11 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             if (!own[j]) continue;
-            if (!BWD || pre) load2<T, V>(y[j], at(s.o_x, j));
-            if (post) load2<T, V>(bs[j], at(s.o_b, j));
+            if (!BWD || pre) q[j].load(y[j], at(s.i_x));
+            if (post) q[j].load(bs[j], at(s.i_b));
             if (gated) {
                 F2 g[H];
-                load2<T, V>(g, at(s.o_g, j));
+                q[j].load(g, at(s.i_g));
                 gate_values<V, sizeof(T) == 2>(p.gate_kind, g, sa[j], da[j]);
 #pragma unroll
                 for (int i = 0; i < H; ++i) sa[j][i] = mul2(sa[j][i], scale);
@@ -540,7 +633,7 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
                     if (post) {
 #pragma unroll
                         for (int i = 0; i < H; ++i) y[j][i] = fma2(sa[j][i], mul2(bs[j][i], s0), y[j][i]);
-                        store2<T, V>(to(p.x_out, j), y[j]);
+                        q[j].store(to(p.x_out), y[j]);
                     }
 #pragma unroll
                     for (int i = 0; i < H; ++i) v = fma2(y[j][i], y[j][i], v);
@@ -554,7 +647,7 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
                     if (own[j]) {
 #pragma unroll
                         for (int i = 0; i < H; ++i) y[j][i] = mul2(mul2(y[j][i], s1), wi[j][i]);
-                        store2<T, V>(to(p.h, j), y[j]);
+                        q[j].store(to(p.h), y[j]);
                     }
             }
             if (p.stats && threadIdx.x == 0) {
@@ -567,7 +660,7 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 if (!own[j]) continue;
-                if (more) load2<T, V>(gx[j], at(s.o_gx, j));
+                if (more) q[j].load(gx[j], at(s.i_gx));
                 else
 #pragma unroll
                     for (int i = 0; i < H; ++i) gx[j][i] = F2(0.f);
@@ -575,7 +668,7 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
 #pragma unroll
                     for (int i = 0; i < H; ++i) bs[j][i] = mul2(bs[j][i], s0);
                 if (pre) {
-                    load2<T, V>(gh[j], at(s.o_gh, j));
+                    q[j].load(gh[j], at(s.i_gh));
 #pragma unroll
                     for (int i = 0; i < H; ++i) {
                         if (post) y[j][i] = fma2(mul2(sa[j][i], wo[j][i]), bs[j][i], y[j][i]);
@@ -600,7 +693,7 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 if (!own[j]) continue;
-                store2<T, V>(to(p.dx, j), gx[j]);
+                q[j].store(to(p.dx), gx[j]);
                 if (!post) continue;
                 F2 dg[H];
 #pragma unroll
@@ -611,7 +704,7 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
                     gx[j][i] = mul2(gx[j][i], mul2(sa[j][i], wo[j][i]));          // q
                     v = fma2(gx[j][i], bs[j][i], v);
                 }
-                if (gated) store2<T, V>(to(p.dgate, j), dg);
+                if (gated) q[j].store(to(p.dgate), dg);
             }
             if (post) {
                 const F2 m2(-(sum(v.sum()) * inv_m));
@@ -621,7 +714,7 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
                     if (own[j]) {
 #pragma unroll
                         for (int i = 0; i < H; ++i) gx[j][i] = mul2(s0, fma2(bs[j][i], m2, gx[j][i]));
-                        store2<T, V>(to(p.db, j), gx[j]);
+                        q[j].store(to(p.db), gx[j]);
                     }
             }
         }
@@ -635,33 +728,42 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
 #pragma unroll
         for (int j = 0; j < J; ++j)
             if (own[j]) {
-                store2<float, V>(part + c0 + j * cstep, dwo[j]);
-                store2<float, V>(part + p.C + c0 + j * cstep, dwi[j]);
+                q[j].store(part, dwo[j]);
+                q[j].store(part + p.C, dwi[j]);
             }
     }
 }
 
 // How a staged launch is cut; slots 0: not staged.
 struct Staged {
-    int V, J, width, threads, slots, nodes, ctas, smem;
+    int V, J, width, threads, slots, nodes, ctas, smem, ring;
     bool row;          // the kernel for wide rows
+    bool apart;        // a thread's channels are `width` apart
 };
 
-// Two slots at least, of what an SM's shared memory holds.
-inline Staged staged_shape(int L, int C, int es, int tensors, bool gated, bool bwd) {
+// Bytes of a tensor's part of a slot: whole 16-byte pieces.
+inline int64_t part_bytes(int64_t bytes, bool apart) { return apart ? (bytes + 30) / 16 * 16 : bytes; }
+
+// Two slots at least, of what an SM's shared memory holds.  tensors: as large
+// as x; gated: the gate too; aligned: all start on 16 bytes.
+inline Staged staged_shape(int L, int C, int es, int tensors, bool gated, bool bwd, bool aligned) {
     Staged s{};
-    const int room = 224 * 1024, wbytes = 2 * (L + 1) * C * 4;
-    const int64_t node = (int64_t)(L + 1) * (L + 1) * C * es * tensors + (gated ? (int64_t)(L + 1) * C * es : 0);
-    if ((int64_t)C * es % 16 != 0) return s;
+    const int room = 224 * 1024, wbytes = (2 * (L + 1) * C * 4 + 15) / 16 * 16;
+    s.apart = !aligned || C * es % 16 != 0;
     s.V = L == 0 ? 16 / es : 4;
     s.J = 1;
-    const int vecs = C / s.V;
+    const int vecs = (C + s.V - 1) / s.V;
+    const auto slot = [&](int nodes) {
+        const int64_t rows = (int64_t)(L + 1) * C * es * nodes;
+        return part_bytes(rows * (L + 1), s.apart) * tensors + (gated ? part_bytes(rows, s.apart) : 0);
+    };
     if (vecs <= 32) {
         s.width = 1;
         while (s.width < vecs) s.width *= 2;
         s.nodes = 32 / s.width;
         s.ctas = 1;
-        const int64_t fit = (room - wbytes) / (node * s.nodes);
+        s.ring = wbytes;
+        const int64_t fit = (room - wbytes) / slot(s.nodes);
         s.slots = (int)(fit < kMaxSlots ? fit : kMaxSlots);
         if (s.slots < 2) return Staged{};
         // Every warp has slots of its own (the slots are a multiple of the warps): a slot's next copies are then
@@ -673,7 +775,7 @@ inline Staged staged_shape(int L, int C, int es, int tensors, bool gated, bool b
         s.slots = s.slots / warps * warps;
         s.threads = 32 * warps;
         // the reduction of the weight gradients takes threads * V floats of the ring
-        if ((int64_t)s.slots * s.nodes * node < (int64_t)s.threads * s.V * 4) return Staged{};
+        if (s.slots * slot(s.nodes) < (int64_t)s.threads * s.V * 4) return Staged{};
     } else if (L == 0) {
         // 8 channels a thread, 16 for the widest 16-bit rows; 512 threads an SM (128 registers each) backward and
         // for the widest, 1024 else
@@ -683,79 +785,76 @@ inline Staged staged_shape(int L, int C, int es, int tensors, bool gated, bool b
         s.width = s.threads = ((vecs + s.J - 1) / s.J + 31) / 32 * 32;
         s.nodes = 1;
         s.ctas = (bwd || s.J * s.V > 8 ? 512 : 1024) / s.threads;
-        int64_t fit = (room / s.ctas - 1536) / node;      // barriers and what the system keeps of each CTA
-        while (fit < 2 && s.ctas > 1) fit = (room / --s.ctas - 1536) / node;
+        int64_t fit = (room / s.ctas - 1536) / slot(1);      // barriers and what the system keeps of each CTA
+        while (fit < 2 && s.ctas > 1) fit = (room / --s.ctas - 1536) / slot(1);
         s.slots = (int)(fit < 4 ? fit : 4);
         if (s.slots < 2) return Staged{};
-        s.smem = (int)node * s.slots;
-        return s;
     } else {
         if (vecs > 256) return Staged{};
         s.width = s.threads = (vecs + 31) / 32 * 32;
         s.nodes = 1;
         s.ctas = 1;
-        const int64_t fit = (room - wbytes) / node;
+        s.ring = wbytes;
+        const int64_t fit = (room - wbytes) / slot(1);
         s.slots = (int)(fit < kMaxSlots ? fit : kMaxSlots);
         if (s.slots < 2) return Staged{};
     }
-    s.smem = wbytes + (int)(node * s.nodes) * s.slots;
+    s.smem = s.ring + (int)slot(s.nodes) * s.slots;
     return s;
 }
 
-template <class T, int V, int L, bool BWD, bool CTA>
+// Lets a kernel have the shared memory of an SM, once per device.
+template <class K>
+cudaError_t allow_smem(K kernel, bool (&done)[64]) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev >= 0 && dev < 64 && done[dev])) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024);
+    if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+    return e;
+}
+
+template <class T, int V, int L, bool BWD, bool CTA, bool APART>
 cudaError_t launch_staged(const StagedParams& s, const Staged& h, int grid, cudaStream_t st) {
     static bool done[64] = {};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    const cudaError_t e = allow_smem(bn_staged_kernel<T, V, L, BWD, CTA, APART>, done);
     if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64 || !done[dev]) {
-        e = cudaFuncSetAttribute(bn_staged_kernel<T, V, L, BWD, CTA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 225 * 1024);
-        if (e != cudaSuccess) return e;
-        if (dev >= 0 && dev < 64) done[dev] = true;
-    }
-    bn_staged_kernel<T, V, L, BWD, CTA><<<grid, h.threads, h.smem, st>>>(s);
+    bn_staged_kernel<T, V, L, BWD, CTA, APART><<<grid, h.threads, h.smem, st>>>(s);
     count_launch();
     return cudaGetLastError();
 }
 
-template <class T, int V, int J, bool BWD>
+template <class T, int V, int J, bool BWD, bool APART>
 cudaError_t launch_row(const StagedParams& s, const Staged& h, int grid, cudaStream_t st) {
     static bool done[64] = {};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    const cudaError_t e = allow_smem(bn_row_kernel<T, V, J, BWD, APART>, done);
     if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64 || !done[dev]) {
-        e = cudaFuncSetAttribute(bn_row_kernel<T, V, J, BWD>, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024);
-        if (e != cudaSuccess) return e;
-        if (dev >= 0 && dev < 64) done[dev] = true;
-    }
-    bn_row_kernel<T, V, J, BWD><<<grid, h.threads, h.smem, st>>>(s);
+    bn_row_kernel<T, V, J, BWD, APART><<<grid, h.threads, h.smem, st>>>(s);
     count_launch();
     return cudaGetLastError();
 }
 
-template <class T, bool BWD>
+template <class T, bool BWD, bool APART>
 cudaError_t staged_for(const StagedParams& s, const Staged& h, int grid, cudaStream_t st) {
     constexpr int W = 16 / sizeof(T);
     const bool cta = h.width > 32;
     if (h.row) {
         if constexpr (W == 8)
-            if (h.J == 1) return launch_row<T, W, 1, BWD>(s, h, grid, st);
-        return launch_row<T, W, 2, BWD>(s, h, grid, st);
+            if (h.J == 1) return launch_row<T, W, 1, BWD, APART>(s, h, grid, st);
+        return launch_row<T, W, 2, BWD, APART>(s, h, grid, st);
     }
     switch (s.p.L) {
         case 0:
-            return launch_staged<T, W, 0, BWD, false>(s, h, grid, st);
+            return launch_staged<T, W, 0, BWD, false, APART>(s, h, grid, st);
         case 1:
-            return cta ? launch_staged<T, 4, 1, BWD, true>(s, h, grid, st)
-                       : launch_staged<T, 4, 1, BWD, false>(s, h, grid, st);
+            return cta ? launch_staged<T, 4, 1, BWD, true, APART>(s, h, grid, st)
+                       : launch_staged<T, 4, 1, BWD, false, APART>(s, h, grid, st);
         case 2:
-            return cta ? launch_staged<T, 4, 2, BWD, true>(s, h, grid, st)
-                       : launch_staged<T, 4, 2, BWD, false>(s, h, grid, st);
+            return cta ? launch_staged<T, 4, 2, BWD, true, APART>(s, h, grid, st)
+                       : launch_staged<T, 4, 2, BWD, false, APART>(s, h, grid, st);
         default:
-            return cta ? launch_staged<T, 4, 3, BWD, true>(s, h, grid, st)
-                       : launch_staged<T, 4, 3, BWD, false>(s, h, grid, st);
+            return cta ? launch_staged<T, 4, 3, BWD, true, APART>(s, h, grid, st)
+                       : launch_staged<T, 4, 3, BWD, false, APART>(s, h, grid, st);
     }
 }
 
