@@ -155,8 +155,8 @@ size_t block_norm_workspace(int L, int C, int N) {
     }
     int64_t ctas = (int64_t)bn::kSMs * most;
     if (ctas > (int64_t)N * (L + 1)) ctas = (int64_t)N * (L + 1);
-    // or, with the sums of all degrees, two CTAs an SM (more for wide rows that need less than an SM's threads)
-    int64_t staged = (int64_t)bn::kSMs * (L == 0 && C < 2048 ? 16 : 2);
+    // or, with the sums of all degrees, one CTA an SM, or several of wide nodes (64 threads at least)
+    int64_t staged = (int64_t)bn::kSMs * (L > 0 ? 4 : C < 2048 ? 16 : 2);
     if (staged > N) staged = N;
     const int64_t r = ctas + L + 1 > staged * (L + 1) ? ctas + L + 1 : staged * (L + 1);
     return (size_t)r * 2 * C * sizeof(float);

@@ -676,14 +676,15 @@ inline Shape shape_of(int L, int C, int V) {
     return s;
 }
 
-// CTAs in proportion to what the degrees move, at least one each and no more
-// than there are batches of nodes.
-inline void split_ctas(BnParams& p, int most, int nodes_per_cta) {
-    const int D = (p.L + 1) * (p.L + 1);
+// CTAs in proportion to the degrees' shares of the time, at least one each and
+// no more than there are batches of nodes.
+inline void split_ctas(BnParams& p, int most, int nodes_per_cta, const float (&share)[4]) {
     const int64_t batches = ((int64_t)p.N + nodes_per_cta - 1) / nodes_per_cta;
+    float all = 0.f;
+    for (int l = 0; l <= p.L; ++l) all += share[l];
     p.first[0] = 0;
     for (int l = 0; l <= p.L; ++l) {
-        int64_t k = (int64_t)most * (2 * l + 1) / D;
+        int64_t k = (int64_t)(most * share[l] / all);
         if (k > batches) k = batches;
         if (k < 1) k = 1;
         p.first[l + 1] = p.first[l] + (int)k;
@@ -713,7 +714,10 @@ cudaError_t launch(BnParams& p, const Shape& s, cudaStream_t st) {
     resident = resident < 1 ? 1 : resident;
     const int cap = cta_cap(s);
     p.width = s.width;
-    split_ctas(p, kSMs * (resident < cap ? resident : cap), s.width <= 32 ? s.threads / s.width : 1);
+    // a batch of nodes takes its rows' time and about that of six rows more, waiting for its loads and sums
+    constexpr int n0 = batch_of<V, 1, J, BWD>(), n1 = batch_of<V, 3, 1, BWD>(), n2 = batch_of<V, 5, 1, BWD>();
+    const float share[4] = {1.f + 6.f / n0, 3.f + 6.f / n1, 5.f + 6.f / n2, 7.f + 6.f};
+    split_ctas(p, kSMs * (resident < cap ? resident : cap), s.width <= 32 ? s.threads / s.width : 1, share);
     kernel<<<p.first[p.L + 1], s.threads, 0, st>>>(p);
     count_launch();
     return cudaGetLastError();

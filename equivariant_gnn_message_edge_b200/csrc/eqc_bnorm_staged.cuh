@@ -744,7 +744,7 @@ struct Staged {
 // Bytes of a tensor's part of a slot: whole 16-byte pieces.
 inline int64_t part_bytes(int64_t bytes, bool apart) { return apart ? (bytes + 30) / 16 * 16 : bytes; }
 
-// Two slots at least, of what an SM's shared memory holds.  tensors: as large
+// Two slots an SM at least, of what its shared memory holds.  tensors: as large
 // as x; gated: the gate too; aligned: all start on 16 bytes.
 inline Staged staged_shape(int L, int C, int es, int tensors, bool gated, bool bwd, bool aligned) {
     Staged s{};
@@ -790,14 +790,17 @@ inline Staged staged_shape(int L, int C, int es, int tensors, bool gated, bool b
         s.slots = (int)(fit < 4 ? fit : 4);
         if (s.slots < 2) return Staged{};
     } else {
+        // one node a CTA; CTAs up to 256 threads an SM backward (up to 255 registers each) and 512 forward, with one
+        // slot each where no more fit: one CTA's copies then run beside the others' work
         if (vecs > 256) return Staged{};
         s.width = s.threads = (vecs + 31) / 32 * 32;
         s.nodes = 1;
-        s.ctas = 1;
         s.ring = wbytes;
-        const int64_t fit = (room - wbytes) / slot(1);
-        s.slots = (int)(fit < kMaxSlots ? fit : kMaxSlots);
-        if (s.slots < 2) return Staged{};
+        const auto slots = [&] { return (room / s.ctas - 1536 - wbytes) / slot(1); };
+        s.ctas = (bwd ? 256 : 512) / s.threads;
+        while (slots() < 1 && s.ctas > 1) --s.ctas;
+        if (slots() < 1 || slots() * s.ctas < 2) return Staged{};
+        s.slots = (int)(slots() < 4 ? slots() : 4);
     }
     s.smem = s.ring + (int)slot(s.nodes) * s.slots;
     return s;
