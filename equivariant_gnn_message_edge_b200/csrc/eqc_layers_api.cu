@@ -200,8 +200,8 @@ int eqconv_embedding_backward(eqconv_plan_t plan, int64_t N, const void* ids, in
     if ((N > 0 && (!gy || !aligned_to(gy, type_bytes(a.out_type)))) || !dtable ||
         !aligned_to(dtable, type_bytes(a.in_type)))
         return EQCONV_ERR_INVALID_ARG;
-    if (!workspace || workspace_bytes < eqc::embed_workspace(a.V, a.C, N) || !aligned_to(workspace, 16))
-        return EQCONV_ERR_WORKSPACE;
+    const size_t need = eqc::embed_workspace(a.V, a.C, N);
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned_to(workspace, 16))) return EQCONV_ERR_WORKSPACE;
     return cuda_status(eqc::embed_backward(a, gy, gy_stride, dtable, workspace, (cudaStream_t)stream),
                        "embedding backward");
 }

@@ -150,13 +150,16 @@ class Embedding:
                 gp, gs = gy.data_ptr(), self.C
             N = ids.numel()
             if out is None:
-                out = torch.empty((self.n_types, self.C), dtype=self.dtype, device=ids.device)
-            dp = _check("out", out, (self.n_types, self.C), self.dtype, self.device)
+                out = gy.new_empty((self.n_types, self.C), dtype=self.dtype)
+                dp = out.data_ptr()
+            else:
+                dp = _check("out", out, (self.n_types, self.C), self.dtype, self.device)
             nbytes = B.eqconv_embedding_workspace_bytes(self.plan, N)
-            if workspace is None:
+            if workspace is None and nbytes:
                 workspace = torch.empty(nbytes, dtype=torch.uint8, device=ids.device)
-            B.eqconv_embedding_backward(self.plan, N, ids.data_ptr(), bits, gp, gs, scale, dp, workspace,
-                                        workspace.numel() * workspace.element_size())
+            if workspace is not None:
+                nbytes = workspace.numel() * workspace.element_size()
+            B.eqconv_embedding_backward(self.plan, N, ids.data_ptr(), bits, gp, gs, scale, dp, workspace, nbytes)
         return out
 
     def __call__(self, ids, table, scale: float = 1.0):
@@ -300,7 +303,7 @@ class _BlockNormFn(torch.autograd.Function):
 
 
 def _tensor_list(grads, out):
-    """(packed array of eqconv_tensor_t, its length, the device's index)"""
+    """(packed array of eqconv_tensor_t, its length, the device's index, the tensors written)"""
     if isinstance(grads, torch.Tensor):
         raise TypeError("expected a list of tensors")
     grads = list(grads)
@@ -332,13 +335,13 @@ def _tensor_list(grads, out):
     at = list(map(torch.Tensor.data_ptr, grads))
     to = at if out is None else list(map(torch.Tensor.data_ptr, outs))
     # four 64-bit words are one eqconv_tensor_t
-    return array.array("q", itertools.chain.from_iterable(zip(at, to, sizes, types))), len(grads), dev
+    return array.array("q", itertools.chain.from_iterable(zip(at, to, sizes, types))), len(grads), dev, outs
 
 
 def gradient_norm(grads, stream=None):
     """sqrt of the sum of all elements' squares, over a list of tensors: a
     0-dimensional fp32 tensor on their device."""
-    arr, n, dev = _tensor_list(grads, None)
+    arr, n, dev, _ = _tensor_list(grads, None)
     with _on(dev, stream):
         rows = arr.buffer_info()[0]
         nbytes = B.eqconv_clip_workspace_bytes(n, rows)
@@ -353,11 +356,12 @@ def clip_gradients(grads, max_norm: float, out=None, eps: float = 1e-6, stream=N
     norm their norm together, in place or into ``out`` (a list of tensors like
     them), and returns norm (a 0-dimensional fp32 tensor).  A tensor may not
     be in the list twice, nor share memory with another."""
-    arr, n, dev = _tensor_list(grads, out)
+    arr, n, dev, outs = _tensor_list(grads, out)
     with _on(dev, stream):
         rows = arr.buffer_info()[0]
         nbytes = B.eqconv_clip_workspace_bytes(n, rows)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=_device(dev))
         norm = ws.new_empty((), dtype=torch.float32)
         B.eqconv_clip_gradients(n, rows, max_norm, eps, norm, ws, nbytes)
+    torch.autograd.graph.increment_version(outs)      # as any in-place operation does
     return norm

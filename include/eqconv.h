@@ -473,7 +473,7 @@ EQCONV_API int eqconv_embedding_plan_create(eqconv_plan_t* out, int64_t n_types,
 EQCONV_API int eqconv_embedding(eqconv_plan_t plan, int64_t N, const void* ids, int id_bits, const void* table,
                                 int64_t table_stride, float scale, void* y, int64_t y_stride, eqconv_stream_t stream);
 
-/* Device workspace bytes eqconv_embedding_backward needs. */
+/* Device workspace bytes eqconv_embedding_backward needs (0: none). */
 EQCONV_API size_t eqconv_embedding_workspace_bytes(eqconv_plan_t plan, int64_t N);
 
 /* dT [n_types][C] (the table's type, contiguous) given gy (out_type, rows

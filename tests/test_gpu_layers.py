@@ -60,6 +60,10 @@ EMBED = [  # N, V, C, table, out, ids
     (20000, 70000, 12, "fp32", "bf16", "int64"),
     (257, 33, 1030, "bf16", "bf16", "int64"),
     (30, 5, 20000, "fp32", "fp32", "int32"),
+    (4096, 296, 32, "fp32", "fp32", "int64"),          # the largest of the one-launch gradient, and just over
+    (4096, 297, 32, "fp16", "fp16", "int32"),
+    (65536, 40, 4, "fp32", "fp32", "int64"),           # the largest one-cluster sort, and just over
+    (65537, 600, 4, "bf16", "bf16", "int32"),
 ]
 
 
@@ -245,6 +249,12 @@ NORM = [  # N, L, C, dtype, gate
     (4000, 0, 96, "bf16", "silu"),
     (6001, 2, 128, "fp32", "silu"),          # dozens of nodes for every warp of every SM
     (5003, 0, 2048, "bf16", "tanh"),
+    (4001, 2, 37, "fp32", "tanh"),           # rows off the 16-byte boundaries
+    (3001, 0, 2047, "fp16", "silu"),
+    (2003, 1, 333, "bf16", "sigmoid"),
+    (1501, 0, 3, "bf16", "none"),
+    (301, 3, 210, "fp32", "silu"),
+    (2, 0, 16384, "fp32", "sigmoid"),
     (20011, 1, 8, "fp16", "sigmoid"),
 ]
 
@@ -406,16 +416,19 @@ def test_block_norm_extreme_gates():
             assert np.abs(np64(a) - w).max() <= 1e-5 * np.abs(w).max() + 1e-6
 
 
-def test_block_norm_unaligned_views():
-    """Tensors that start off the 16-byte boundary give the aligned ones' results."""
-    N, L, C = 21, 1, 64
+@pytest.mark.parametrize("N,L,C", [(21, 1, 64), (100, 1, 7), (1, 0, 1), (40, 0, 3), (9, 0, 4001), (700, 2, 33)])
+def test_block_norm_unaligned_views(N, L, C):
+    """Tensors that start off the 16-byte boundary, each by its own step, give
+    the aligned ones' results: the bytes before and behind them are NaN."""
     args = _norm_case(N, L, C, "bf16", "silu", seed=6)
     op = layers.BlockNorm(natural_irreps(L), C, gate="silu", dtype=torch.bfloat16)
+    steps = iter(range(1, 100))
 
     def off(t):
-        room = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
-        room[1:] = t.reshape(-1)
-        return room[1:].view(t.shape)
+        k = next(steps) % 7 + 1
+        room = torch.full((t.numel() + 2 * k,), float("nan"), dtype=t.dtype, device="cuda")
+        room[k:-k] = t.reshape(-1)
+        return room[k:-k].view(t.shape)
 
     a = op.forward_raw(*args[:5], save=True)
     o = [off(t) for t in args]
@@ -610,10 +623,10 @@ def test_clip_refusals():
 
 # --------------------------------------------------------- streams and graphs
 
-def test_own_stream_and_graph_replay():
+@pytest.mark.parametrize("N,L,C,V", [(700, 1, 64, 50), (9000, 0, 33, 3000), (70000, 1, 8, 1000)])
+def test_own_stream_and_graph_replay(N, L, C, V):
     """On a stream of their own, and captured: replays follow the inputs'
     current contents, and two graphs share no workspace."""
-    N, L, C, V = 700, 1, 64, 50
     s = torch.cuda.Stream()
     emb, norm = layers.Embedding(V, C), layers.BlockNorm(natural_irreps(L), C)
     z, table, gy = _embed_case(N, V, C, "fp32", "fp32", "int32")
@@ -648,6 +661,43 @@ def test_own_stream_and_graph_replay():
     want = step()
     for r in results:
         assert all(torch.equal(a, c) for a, c in zip(r, want))
+
+
+def test_two_streams_at_once():
+    """Calls of one operator that overlap on two streams do not disturb each other."""
+    V, C, L = 5000, 64, 1
+    emb, norm = layers.Embedding(V, C), layers.BlockNorm(natural_irreps(L), C)
+    cases = [(_embed_case(30000, V, C, "fp32", "fp32", "int64", seed=k), _norm_case(3000, L, C, "fp32", "sigmoid", seed=k),
+              _tensors([100000, 77], ["fp32", "bf16"], seed=k)) for k in range(2)]
+
+    def run(k):
+        (z, table, gy), (x, b, gate, wo, wi, gx, gh), ts = cases[k]
+        outs = [torch.empty_like(t) for t in ts]
+        _, _, st = norm.forward_raw(x, b, gate, wo, wi, save=True)
+        return [emb.backward_raw(z, gy), *norm.backward_raw(x, b, gate, wo, wi, st, gx, gh),
+                layers.clip_gradients(ts, 0.1, out=outs), *outs]
+
+    want = [[t.clone() for t in run(k)] for k in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append((k, run(k)))
+    torch.cuda.synchronize()
+    for k, r in got:
+        assert all(torch.equal(a, c) for a, c in zip(r, want[k]))
+
+
+def test_clip_counts_as_in_place():
+    """Autograd notices that a tensor it saved was clipped in place."""
+    w = randn(gen(1), 50).requires_grad_(True)
+    y = w * 2
+    z = (y * y).sum()
+    layers.clip_gradients([y.detach()], 1e-3)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        z.backward()
 
 
 def test_training_step_of_two_layers():
