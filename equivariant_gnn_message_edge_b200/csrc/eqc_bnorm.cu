@@ -18,6 +18,7 @@ namespace {
 // block's 8 warps and the warps' sums in order.  rows: degrees a CTA has sums
 // of (L + 1, or 1 where CTAs first[l] .. first[l + 1] work on degree l).
 __global__ void __launch_bounds__(256) bn_dw_reduce(const BnParams p, int rows, float* dw_post, float* dw_pre) {
+    wait_for_last();
     __shared__ float s[8][32];
     const int x = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + x, l = blockIdx.y;
     float* dw = blockIdx.z ? dw_pre : dw_post;
@@ -173,9 +174,9 @@ cudaError_t block_norm_backward(const BlockNormArgs& a, cudaStream_t st) {
     bn::BnParams p = bn::params_of(a);
     int rows = 0;
     if ((err = bn::run(p, a, true, st, &rows)) != cudaSuccess || (!a.dw_post && !a.dw_pre)) return err;
-    bn::bn_dw_reduce<<<dim3((a.C + 31) / 32, a.L + 1, 2), 256, 0, st>>>(p, rows, a.dw_post, a.dw_pre);
+    err = launch_after(bn::bn_dw_reduce, dim3((a.C + 31) / 32, a.L + 1, 2), 256, st, p, rows, a.dw_post, a.dw_pre);
     count_launch();
-    return cudaGetLastError();
+    return err;
 }
 
 }  // namespace eqc

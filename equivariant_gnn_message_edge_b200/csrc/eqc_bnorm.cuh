@@ -219,6 +219,7 @@ __global__ void __launch_bounds__(256) bn_fwd_stream(const BnParams p) {
 // shared memory, each channel by the thread that owns it.
 template <class T>
 __global__ void __launch_bounds__(256) bn_bwd_stream(const BnParams p) {
+    let_next_start();
     extern __shared__ float acc[];   // [2][C]
     __shared__ float red[8];
     const int l = degree_of(p, blockIdx.x), K = 2 * l + 1, D = (p.L + 1) * (p.L + 1);
@@ -640,6 +641,7 @@ __global__ void __launch_bounds__(LMAX == 0 ? 512 : 256) bn_fwd_kernel(const BnP
 
 template <class T, int V, int LMAX, int J>
 __global__ void __launch_bounds__(LMAX == 0 ? 512 : 256) bn_bwd_kernel(const BnParams p) {
+    let_next_start();
     __shared__ float red[2 * 4 * 16];
     __shared__ float dw[128 * 2 * V];
     const int l = degree_of(p, blockIdx.x);

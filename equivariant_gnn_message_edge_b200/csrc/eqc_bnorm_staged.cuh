@@ -384,6 +384,7 @@ __device__ __forceinline__ void bwd_node(const BnParams& p, const View<T>& s, co
 // Shared memory: [w_post, w_pre: 2 (L + 1) C floats] [ring of slots].
 template <class T, int V, int L, bool BWD, bool CTA, bool APART>
 __global__ void __launch_bounds__(CTA ? 256 : BWD ? 256 : 512, 1) bn_staged_kernel(const StagedParams s) {
+    if constexpr (BWD) let_next_start();
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ uint64_t full[kMaxSlots];
     __shared__ float red[CTA ? 2 * (L + 1) * 16 : 1];
@@ -531,6 +532,7 @@ struct CtaSum {
 
 template <class T, int V, int J, bool BWD, bool APART>
 __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(const StagedParams s) {
+    if constexpr (BWD) let_next_start();
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ uint64_t full[kMaxSlots];
     __shared__ __align__(16) float red[2 * 16];

@@ -150,6 +150,7 @@ __device__ __forceinline__ void scale_chunk(const void* base, void* out_, int64_
 // part[first + block] = sum of squares of the block's chunks.
 template <int MAXT>
 __global__ void __launch_bounds__(kThreads, kNormPerSm) clip_norm_kernel(const __grid_constant__ Table<MAXT> t, double* part) {
+    let_next_start();
     __shared__ double red[kThreads / 32];
     double s = 0.0;
     for (int chunk = blockIdx.x; chunk < t.chunk0[t.count]; chunk += gridDim.x) {
@@ -169,6 +170,7 @@ __device__ __forceinline__ double total_norm(const double* part, int parts, doub
 }
 
 __global__ void __launch_bounds__(kThreads) clip_total_kernel(const double* part, int parts, float* norm) {
+    wait_for_last();
     __shared__ double red[kThreads / 32];
     const double n = total_norm(part, parts, red);
     if (threadIdx.x == 0) *norm = (float)n;
@@ -178,6 +180,8 @@ template <int MAXT>
 __global__ void __launch_bounds__(kThreads, kScalePerSm) clip_scale_kernel(const __grid_constant__ Table<MAXT> t,
                                                               const double* part, int parts, float max_norm,
                                                               float eps, float* norm) {
+    wait_for_last();
+    let_next_start();
     __shared__ double red[kThreads / 32];
     const double n = total_norm(part, parts, red);
     if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)n;
@@ -242,18 +246,19 @@ cudaError_t run(int n, const eqconv_tensor_t* ts, bool scale, float max_norm, fl
         ++tables;
     }
     if (!scale || tables == 0) {
-        clip_total_kernel<<<1, kThreads, 0, st>>>(part, parts, norm);
+        const cudaError_t err = launch_after(clip_total_kernel, 1, kThreads, st, part, parts, norm);
         count_launch();
-        return cudaGetLastError();
+        return err == cudaSuccess ? cudaGetLastError() : err;
     }
     bool first = true;
     for (int from = 0; from < n;) {
         if (tables > 1) from = fill(t, n, ts, from);
         else from = n;
         if (t.count == 0) continue;
-        clip_scale_kernel<MAXT><<<blocks_for(t.chunk0[t.count], kScalePerSm), kThreads, 0, st>>>(
-            t, part, parts, max_norm, eps, first ? norm : nullptr);
+        const cudaError_t err = launch_after(clip_scale_kernel<MAXT>, blocks_for(t.chunk0[t.count], kScalePerSm), kThreads,
+                                             st, t, part, parts, max_norm, eps, first ? norm : nullptr);
         count_launch();
+        if (err != cudaSuccess) return err;
         first = false;
     }
     return cudaGetLastError();

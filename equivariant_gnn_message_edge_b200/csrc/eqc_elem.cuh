@@ -162,6 +162,27 @@ __device__ __forceinline__ void store2(T* p, const F2 (&v)[V / 2]) {
     }
 }
 
+// Kernels of one call that follow one another: the next one's CTAs may take
+// their places on the SMs while the last CTAs of this one still run
+// (let_next_start), and wait there until it has ended and its writes are seen
+// (wait_for_last, before anything else).  launch_after starts such a next one.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;"); }
+__device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <class... P, class... A>
+inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t st, A&&... args) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // Bytes of one element of a type code (0: unknown code).
 inline int type_bytes(int code) { return code == 0 ? 4 : (code == 1 || code == 2) ? 2 : 0; }
 

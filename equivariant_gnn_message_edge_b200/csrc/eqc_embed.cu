@@ -167,6 +167,7 @@ template <class ID, int ROUNDS>
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const void* ids, int N, int64_t V, int64_t padding,
                                                                   int digit_bits, int passes, int* keys, int* perm,
                                                                   uint4* zero, int64_t zeros, unsigned* status) {
+    let_next_start();
     extern __shared__ __align__(16) unsigned char smem_raw[];
     SortSmem<ROUNDS>& s = *reinterpret_cast<SortSmem<ROUNDS>*>(smem_raw);
     cg::cluster_group cluster = cg::this_cluster();
@@ -271,6 +272,8 @@ template <class ID, bool FIRST>
 __global__ void __launch_bounds__(kLsdThreads) embed_hist_kernel(const void* in, int N, int64_t V, int64_t padding,
                                                                  int shift, int mask, int* hist, int tiles,
                                                                  unsigned* status) {
+    wait_for_last();
+    let_next_start();
     __shared__ int h[kRadix];
     h[threadIdx.x] = 0;
     __syncthreads();
@@ -291,6 +294,8 @@ __global__ void __launch_bounds__(kLsdThreads) embed_hist_kernel(const void* in,
 
 // hist[d][*] becomes its exclusive scan over the tiles, total[d] its sum: one warp per digit.
 __global__ void embed_scan_kernel(int* hist, int tiles, int radix, int* total) {
+    wait_for_last();
+    let_next_start();
     const int d = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
     if (d >= radix) return;
     int* h = hist + (int64_t)d * tiles;
@@ -314,6 +319,8 @@ __global__ void __launch_bounds__(kLsdThreads) embed_scatter_kernel(const void* 
                                                                     int64_t V, int64_t padding, int shift, int mask,
                                                                     const int* hist, const int* total, int tiles,
                                                                     int* keys_out, int* idx_out, unsigned* status) {
+    wait_for_last();
+    let_next_start();
     __shared__ int wh[kLsdThreads / 32][kRadix];
     __shared__ int base[kRadix];
     __shared__ int sums[kLsdThreads / 32];
@@ -382,6 +389,8 @@ __device__ __forceinline__ int lower_bound(const int* keys, int n, int k) {
 // ordered keys show by search.  Bound by memory: gy is read once, dT written once.
 template <class T, class O, int VE>
 __global__ void __launch_bounds__(256) embed_sum_kernel(const SumParams p, const O* gy, T* dtable) {
+    wait_for_last();
+    let_next_start();
     if ((int)blockIdx.x >= p.sum_blocks) {
         __shared__ bool empty[kZeroRows];
         const int64_t v0 = p.zero_from + (int64_t)(blockIdx.x - p.sum_blocks) * p.zero_rows;
@@ -478,6 +487,7 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const SumParams p, const
 // and the workers' sums in order.
 template <class T, int VE>
 __global__ void __launch_bounds__(256) embed_join_kernel(const SumParams p, T* dtable) {
+    wait_for_last();
     const int tile = blockIdx.x, slab = blockIdx.y;
     const int64_t end = (int64_t)(tile + 1) * p.R;       // < N for every tile of the grid
     const int k = __ldg(p.keys + end - 1);
@@ -734,23 +744,22 @@ cudaError_t sort_in_tiles(const EmbedArgs& a, int digit_bits, int passes, char* 
     const int tiles = cdiv(a.N, kLsdTile), radix = 1 << digit_bits, N = (int)a.N;
     for (int p = 0; p < passes; ++p) {
         const int shift = p * digit_bits, o = p & 1;
+        // (the first kernel of the call starts when all work before it has ended, as any launch does)
+        cudaError_t err = cudaSuccess;
         if (p == 0)
             embed_hist_kernel<ID, true><<<tiles, kLsdThreads, 0, st>>>(a.ids, N, a.V, a.padding, shift, radix - 1,
                                                                        hist, tiles, a.status);
         else
-            embed_hist_kernel<ID, false><<<tiles, kLsdThreads, 0, st>>>(k[o ^ 1], N, a.V, a.padding, shift, radix - 1,
-                                                                        hist, tiles, a.status);
-        embed_scan_kernel<<<cdiv(radix, 8), 256, 0, st>>>(hist, tiles, radix, total);
-        if (p == 0)
-            embed_scatter_kernel<ID, true><<<tiles, kLsdThreads, 0, st>>>(a.ids, nullptr, N, a.V, a.padding, shift,
-                                                                          radix - 1, hist, total, tiles, k[o], x[o],
-                                                                          a.status);
-        else
-            embed_scatter_kernel<ID, false><<<tiles, kLsdThreads, 0, st>>>(k[o ^ 1], x[o ^ 1], N, a.V, a.padding,
-                                                                           shift, radix - 1, hist, total, tiles, k[o],
-                                                                           x[o], a.status);
+            err = launch_after(embed_hist_kernel<ID, false>, tiles, kLsdThreads, st, k[o ^ 1], N, a.V, a.padding, shift,
+                               radix - 1, hist, tiles, a.status);
+        if (err == cudaSuccess) err = launch_after(embed_scan_kernel, cdiv(radix, 8), 256, st, hist, tiles, radix, total);
+        if (err == cudaSuccess)
+            err = p == 0 ? launch_after(embed_scatter_kernel<ID, true>, tiles, kLsdThreads, st, a.ids, nullptr, N, a.V,
+                                        a.padding, shift, radix - 1, hist, total, tiles, k[o], x[o], a.status)
+                         : launch_after(embed_scatter_kernel<ID, false>, tiles, kLsdThreads, st, k[o ^ 1], x[o ^ 1], N,
+                                        a.V, a.padding, shift, radix - 1, hist, total, tiles, k[o], x[o], a.status);
         for (int i = 0; i < 3; ++i) count_launch();
-        const cudaError_t err = cudaGetLastError();
+        if (err == cudaSuccess) err = cudaGetLastError();
         if (err != cudaSuccess) return err;
         *keys = k[o];
         *perm = x[o];
@@ -841,14 +850,15 @@ cudaError_t embed_backward(const EmbedArgs& a, const void* gy, int64_t gy_stride
                 const int64_t zr = kZeroBytes / row;
                 p.zero_from = zero_to;
                 p.zero_rows = (int)(zr < 1 ? 1 : zr > kZeroRows ? kZeroRows : zr);
-                embed_sum_kernel<T, O, VE><<<p.sum_blocks + cdiv(a.V - zero_to, p.zero_rows), 256, 0, st>>>(
-                    p, static_cast<const O*>(gy), static_cast<T*>(dtable));
+                cudaError_t e = launch_after(embed_sum_kernel<T, O, VE>, p.sum_blocks + cdiv(a.V - zero_to, p.zero_rows),
+                                             256, st, p, static_cast<const O*>(gy), static_cast<T*>(dtable));
                 count_launch();
-                if (s.tiles > 1) {
-                    embed_join_kernel<T, VE><<<dim3(s.tiles - 1, s.slabs), 256, 0, st>>>(p, static_cast<T*>(dtable));
+                if (e == cudaSuccess && s.tiles > 1) {
+                    e = launch_after(embed_join_kernel<T, VE>, dim3(s.tiles - 1, s.slabs), 256, st, p,
+                                     static_cast<T*>(dtable));
                     count_launch();
                 }
-                return cudaGetLastError();
+                return e;
             });
         });
     });
