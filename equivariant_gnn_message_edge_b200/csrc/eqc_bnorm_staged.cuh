@@ -228,70 +228,81 @@ __device__ __forceinline__ void fwd_node(const BnParams& p, const View<T>& s, co
         }
 }
 
-// kKeep (fp32): t goes into the slot in the place of g_h, so that db needs no
-// second pass over x, g_x and g_h; 16 bits would round it, so it is made again.
+// With f = scale a(gate) w_post, bs = b s_b and p = g_h w_pre, the mean that db
+// needs is linear in the mean that t needs:
+//   sum f bs t = sum f bs (g_x + s_y p) - s_y m1 sum f bs y,   m1 = s_y^2 mean(p y)
+// so one round of sums serves both, and t, dx and db follow in one pass.
 template <class T, int V, int L, bool APART>
 __device__ __forceinline__ void bwd_node(const BnParams& p, const View<T>& s, const float* w, const Lanes<V, APART>& q,
                                          bool own, bool live, int64_t row, int64_t grow, const float (&sb)[L + 1],
                                          const float (&sy)[L + 1], F2 (&dwo)[L + 1][V / 2], F2 (&dwi)[L + 1][V / 2],
-                                         WorkerSum<L + 1>& sum) {
+                                         WorkerSum<3 * (L + 1)>& sum) {
     constexpr int H = V / 2;
-    constexpr bool kKeep = sizeof(T) == 4;
     const bool post = p.b != nullptr, pre = p.g_h != nullptr, gated = p.gate != nullptr, more = p.g_x != nullptr;
     F2 sa[L + 1][H], da[L + 1][H];     // scale a(gate), scale a'(gate)
-    float mpy[L + 1], mqb[L + 1];
-    // y of a row: x + k b with k = sa sb w_post
-    const auto y_of = [&](int r, const F2 (&k)[H], const F2 (&b)[H], F2 (&y)[H]) {
-        q.load(y, s.x + r * p.C);
-        if (post)
-#pragma unroll
-            for (int i = 0; i < H; ++i) y[i] = fma2(k[i], b[i], y[i]);
-    };
+    float sums[3 * (L + 1)];           // per degree: p y, f bs y, f bs (g_x + s_y p)
 #pragma unroll
     for (int l = 0; l <= L; ++l) {
-        mpy[l] = mqb[l] = 0.f;
+        sums[3 * l] = sums[3 * l + 1] = sums[3 * l + 2] = 0.f;
         if (!own) continue;
         if (gated) {
             F2 g[H];
             q.load(g, s.g + l * p.C);
             gate_values<V, sizeof(T) == 2>(p.gate_kind, g, sa[l], da[l]);
         }
+        F2 wi[H], k[H], v0(0.f), v1(0.f), v2(0.f);
+        if (pre) q.load(wi, w + (L + 1 + l) * p.C);
+        if (post) q.load(k, w + l * p.C);
 #pragma unroll
         for (int i = 0; i < H; ++i) {
             sa[l][i] = gated ? mul2(sa[l][i], F2(p.scale)) : F2(p.scale);
             da[l][i] = gated ? mul2(da[l][i], F2(p.scale)) : F2(0.f);
-        }
-        if (!pre) continue;
-        F2 wi[H], k[H], b[H], v(0.f);
-        q.load(wi, w + (L + 1 + l) * p.C);
-        if (post) {
-            q.load(k, w + l * p.C);
-#pragma unroll
-            for (int i = 0; i < H; ++i) k[i] = mul2(mul2(k[i], sa[l][i]), F2(sb[l]));
+            if (post) k[i] = mul2(mul2(k[i], sa[l][i]), F2(sb[l]));
         }
 #pragma unroll
         for (int m = 0; m < 2 * l + 1; ++m) {
-            F2 gh[H], y[H];
-            if (post) q.load(b, s.b + (l * l + m) * p.C);
-            y_of(l * l + m, k, b, y);
-            q.load(gh, s.gh + (l * l + m) * p.C);
+            const int r = l * l + m;
+            F2 b[H], t[H];
+            if (post) q.load(b, s.b + r * p.C);
+            if (post && more) q.load(t, s.gx + r * p.C);
+            else
 #pragma unroll
-            for (int i = 0; i < H; ++i) v = fma2(mul2(gh[i], wi[i]), y[i], v);
+                for (int i = 0; i < H; ++i) t[i] = F2(0.f);
+            if (pre) {
+                F2 gh[H], y[H];
+                q.load(y, s.x + r * p.C);
+                q.load(gh, s.gh + r * p.C);
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    const F2 pp = mul2(gh[i], wi[i]);
+                    if (post) {
+                        const F2 fb = mul2(k[i], b[i]);
+                        y[i] = add2(fb, y[i]);
+                        v1 = fma2(fb, y[i], v1);
+                        v2 = fma2(fb, fma2(pp, F2(sy[l]), t[i]), v2);
+                    }
+                    v0 = fma2(pp, y[i], v0);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < H; ++i) v2 = fma2(mul2(k[i], b[i]), t[i], v2);
+            }
         }
-        mpy[l] = v.sum();
+        sums[3 * l] = v0.sum();
+        sums[3 * l + 1] = v1.sum();
+        sums[3 * l + 2] = v2.sum();
     }
-    if (pre) {
-        sum(mpy);
-#pragma unroll
-        for (int l = 0; l <= L; ++l) mpy[l] *= sy[l] * sy[l] * sy[l] * (1.f / ((2 * l + 1) * (float)p.C));
-    }
+    sum(sums);
 #pragma unroll
     for (int l = 0; l <= L; ++l) {
         if (!own) continue;
-        F2 wi[H], wo[H], k[H], tb[H], gy[H];      // wi: sy w_pre
+        const float inv_m = 1.f / ((2 * l + 1) * (float)p.C);
+        const float m1 = sums[3 * l] * inv_m * sy[l] * sy[l] * sy[l];           // with t's factor s_y
+        const float m2 = (sums[3 * l + 2] - m1 * sums[3 * l + 1]) * inv_m * sb[l] * sb[l];
+        F2 wi[H], wo[H], k[H], tb[H], gy[H];      // wi: s_y w_pre
         if (pre) q.load(wi, w + (L + 1 + l) * p.C);
         if (post) q.load(wo, w + l * p.C);
-        const F2 m1(-mpy[l]), s1(sy[l]), s0(sb[l]);
+        const F2 n1(-m1), n2(-m2), s1(sy[l]), s0(sb[l]);
 #pragma unroll
         for (int i = 0; i < H; ++i) {
             tb[i] = gy[i] = F2(0.f);
@@ -309,75 +320,36 @@ __device__ __forceinline__ void bwd_node(const BnParams& p, const View<T>& s, co
                 for (int i = 0; i < H; ++i) t[i] = F2(0.f);
             if (pre) {
                 F2 gh[H], y[H];
-                y_of(r, k, b, y);
+                q.load(y, s.x + r * p.C);
                 q.load(gh, s.gh + r * p.C);
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
-                    t[i] = fma2(gh[i], wi[i], fma2(y[i], m1, t[i]));
+                    if (post) y[i] = fma2(k[i], b[i], y[i]);
+                    t[i] = fma2(gh[i], wi[i], fma2(y[i], n1, t[i]));
                     gy[i] = fma2(gh[i], y[i], gy[i]);
                 }
-                if constexpr (kKeep)
-                    if (post) q.store(const_cast<T*>(s.gh) + r * p.C, t);
             }
-            if (post)
-#pragma unroll
-                for (int i = 0; i < H; ++i) tb[i] = fma2(t[i], b[i], tb[i]);
             if (live) q.store(static_cast<T*>(p.dx) + row + r * p.C, t);
+            if (post) {
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    tb[i] = fma2(t[i], b[i], tb[i]);
+                    t[i] = fma2(k[i], t[i], mul2(b[i], n2));
+                }
+                if (live) q.store(static_cast<T*>(p.db) + row + r * p.C, t);
+            }
         }
-        F2 v(0.f), dg[H];
+        F2 dg[H];
 #pragma unroll
         for (int i = 0; i < H; ++i) {
             if (post) {
                 const F2 u = mul2(tb[i], s0);
-                v = fma2(mul2(sa[l][i], wo[i]), tb[i], v);
                 if (live) dwo[l][i] = fma2(sa[l][i], u, dwo[l][i]);
                 dg[i] = mul2(mul2(da[l][i], wo[i]), u);
             }
             if (live && pre) dwi[l][i] = fma2(gy[i], s1, dwi[l][i]);
         }
-        mqb[l] = v.sum();
         if (gated && live) q.store(static_cast<T*>(p.dgate) + grow + l * p.C, dg);
-    }
-    if (!post) return;
-    sum(mqb);
-#pragma unroll
-    for (int l = 0; l <= L; ++l) {
-        mqb[l] *= sb[l] * sb[l] * sb[l] * (1.f / ((2 * l + 1) * (float)p.C));
-        if (!own) continue;
-        F2 wi[H], k[H];
-        const F2 m1(-mpy[l]), m2(-mqb[l]);
-        q.load(k, w + l * p.C);
-#pragma unroll
-        for (int i = 0; i < H; ++i) k[i] = mul2(mul2(k[i], sa[l][i]), F2(sb[l]));
-        if (pre && !kKeep) {
-            q.load(wi, w + (L + 1 + l) * p.C);
-#pragma unroll
-            for (int i = 0; i < H; ++i) wi[i] = mul2(wi[i], F2(sy[l]));
-        }
-#pragma unroll
-        for (int m = 0; m < 2 * l + 1; ++m) {
-            const int r = l * l + m;
-            F2 t[H], b[H];
-            q.load(b, s.b + r * p.C);
-            if (pre && kKeep) {
-                q.load(t, s.gh + r * p.C);
-            } else {
-                if (more) q.load(t, s.gx + r * p.C);
-                else
-#pragma unroll
-                    for (int i = 0; i < H; ++i) t[i] = F2(0.f);
-                if (pre) {
-                    F2 gh[H], y[H];
-                    y_of(r, k, b, y);
-                    q.load(gh, s.gh + r * p.C);
-#pragma unroll
-                    for (int i = 0; i < H; ++i) t[i] = fma2(gh[i], wi[i], fma2(y[i], m1, t[i]));
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < H; ++i) t[i] = fma2(k[i], t[i], mul2(b[i], m2));
-            if (live) q.store(static_cast<T*>(p.db) + row + r * p.C, t);
-        }
     }
 }
 
@@ -387,7 +359,7 @@ __global__ void __launch_bounds__(CTA ? 256 : BWD ? 256 : 512, 1) bn_staged_kern
     if constexpr (BWD) let_next_start();
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ uint64_t full[kMaxSlots];
-    __shared__ float red[CTA ? 2 * (L + 1) * 16 : 1];
+    __shared__ float red[CTA ? 2 * (BWD ? 3 : 1) * (L + 1) * 16 : 1];
     constexpr int D = (L + 1) * (L + 1);
     const BnParams& p = s.p;
     float* w = reinterpret_cast<float*>(smem);
@@ -414,7 +386,7 @@ __global__ void __launch_bounds__(CTA ? 256 : BWD ? 256 : 512, 1) bn_staged_kern
     for (int l = 0; l < (BWD ? L + 1 : 1); ++l)
 #pragma unroll
         for (int i = 0; i < V / 2; ++i) dwo[l][i] = dwi[l][i] = F2(0.f);
-    WorkerSum<L + 1> sum{red, width, 0};
+    WorkerSum<BWD ? 3 * (L + 1) : L + 1> sum{red, width, 0};
     const int mine = s.total > blockIdx.x ? (int)((s.total - blockIdx.x + gridDim.x - 1) / gridDim.x) : 0;
     bool ok = true;
     // a node's statistics are fetched while the worker's last node is worked on
@@ -460,8 +432,7 @@ __global__ void __launch_bounds__(CTA ? 256 : BWD ? 256 : 512, 1) bn_staged_kern
             bwd_node<T, V, L, APART>(p, v, w, q, own, live, row, grow, sb, sy, dwo, dwi, sum);
         else
             fwd_node<T, V, L, APART>(p, v, w, q, own, live, row, n * (L + 1), x0 == 0, sum);
-        // everyone has read (and written) the slot: its next copies may come
-        if constexpr (BWD && sizeof(T) == 4) bulk::fence_writes();
+        // everyone has read the slot: its next copies may come
         if constexpr (CTA) __syncthreads();
         else __syncwarp();
         if (lane < 32) fill(s, ring, k + s.slots, lane);
@@ -510,23 +481,31 @@ __global__ void __launch_bounds__(CTA ? 256 : BWD ? 256 : 512, 1) bn_staged_kern
 // bounds it, beside memory, is the instructions per element, so every factor
 // of a channel is formed once and the weights stay in registers.
 
-// The sum of v over the CTA; red: [2][16], zeros behind the last warp.
+// Sums of K values over the CTA; red: [2][K][16], zeros behind the last warp.
+template <int K>
 struct CtaSum {
     float* red;
     int flip;
-    __device__ __forceinline__ float operator()(float v) {
+    __device__ __forceinline__ void operator()(float (&v)[K]) {
 #pragma unroll
-        for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        float* r = red + flip * 16;
-        flip ^= 1;       // the next sum's buffer: one barrier a sum is enough
-        if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = v;
+        for (int o = 16; o; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < K; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        float* r = red + flip * K * 16;
+        flip ^= 1;       // the next sums' buffer: one barrier a round is enough
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int i = 0; i < K; ++i) r[i * 16 + (threadIdx.x >> 5)] = v[i];
         __syncthreads();
-        F2 q[4][2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) load2<float, 4>(q[i], r + 4 * i);
-        return add2(add2(add2(q[0][0], q[0][1]), add2(q[1][0], q[1][1])),
-                    add2(add2(q[2][0], q[2][1]), add2(q[3][0], q[3][1])))
-            .sum();
+        for (int i = 0; i < K; ++i) {
+            F2 q[4][2];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) load2<float, 4>(q[j], r + i * 16 + 4 * j);
+            v[i] = add2(add2(add2(q[0][0], q[0][1]), add2(q[1][0], q[1][1])),
+                        add2(add2(q[2][0], q[2][1]), add2(q[3][0], q[3][1])))
+                       .sum();
+        }
     }
 };
 
@@ -535,13 +514,14 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
     if constexpr (BWD) let_next_start();
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ uint64_t full[kMaxSlots];
-    __shared__ __align__(16) float red[2 * 16];
+    constexpr int K = BWD ? 3 : 1;
+    __shared__ __align__(16) float red[2 * K * 16];
     const BnParams& p = s.p;
     const Ring ring{smem, full};
     const bool post = p.b != nullptr, gated = p.gate != nullptr;
     const bool pre = BWD ? p.g_h != nullptr : p.w_pre != nullptr, more = p.g_x != nullptr;
     const float inv_m = 1.f / (float)p.C;
-    if (threadIdx.x < 32) red[threadIdx.x] = 0.f;
+    for (int i = threadIdx.x; i < 2 * K * 16; i += blockDim.x) red[i] = 0.f;
     if (threadIdx.x == 0) {
         for (int i = 0; i < s.slots; ++i) bulk::init(full + i, s.tensors);
         bulk::fence_init();
@@ -563,7 +543,7 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
 #pragma unroll
         for (int i = 0; i < H; ++i) dwo[j][i] = dwi[j][i] = F2(0.f);
     }
-    CtaSum sum{red, 0};
+    CtaSum<K> sum{red, 0};
     const F2 scale(p.scale);
     const int mine = s.total > blockIdx.x ? (int)((s.total - blockIdx.x + gridDim.x - 1) / gridDim.x) : 0;
     // a row's statistics are fetched while the row before is worked on
@@ -624,7 +604,9 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
                             v = fma2(bs[j][i], bs[j][i], v);
                             sa[j][i] = mul2(sa[j][i], wo[j][i]);
                         }
-                sb = rsqrtf(sum(v.sum()) * inv_m + p.eps);
+                float total[1] = {v.sum()};
+                if constexpr (!BWD) sum(total);
+                sb = rsqrtf(total[0] * inv_m + p.eps);
                 release();
             }
             F2 v(0.f);
@@ -641,7 +623,9 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
                     for (int i = 0; i < H; ++i) v = fma2(y[j][i], y[j][i], v);
                 }
             if (pre) {
-                sy = rsqrtf(sum(v.sum()) * inv_m + p.eps);
+                float total[1] = {v.sum()};
+                if constexpr (!BWD) sum(total);
+                sy = rsqrtf(total[0] * inv_m + p.eps);
                 if (!post) release();
                 const F2 s1(sy);
 #pragma unroll
@@ -657,7 +641,8 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
                 if (pre) p.stats[p.N + n] = sy;
             }
         } else {
-            F2 gx[J][H], gh[J][H], v(0.f);
+            // one round of sums, as in bwd_node: p y, f bs y, f bs (g_x + s_y p)
+            F2 gx[J][H], gh[J][H], v0(0.f), v1(0.f), v2(0.f);
             const F2 s0(sb), s1(sy);
 #pragma unroll
             for (int j = 0; j < J; ++j) {
@@ -666,35 +651,39 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
                 else
 #pragma unroll
                     for (int i = 0; i < H; ++i) gx[j][i] = F2(0.f);
-                if (post)
+                if (pre) q[j].load(gh[j], at(s.i_gh));
 #pragma unroll
-                    for (int i = 0; i < H; ++i) bs[j][i] = mul2(bs[j][i], s0);
-                if (pre) {
-                    q[j].load(gh[j], at(s.i_gh));
-#pragma unroll
-                    for (int i = 0; i < H; ++i) {
-                        if (post) y[j][i] = fma2(mul2(sa[j][i], wo[j][i]), bs[j][i], y[j][i]);
-                        const F2 gy = mul2(gh[j][i], y[j][i]);
-                        v = fma2(gy, wi[j][i], v);
-                        dwi[j][i] = fma2(gy, s1, dwi[j][i]);
+                for (int i = 0; i < H; ++i) {
+                    F2 fb;
+                    if (post) {
+                        bs[j][i] = mul2(bs[j][i], s0);
+                        fb = mul2(mul2(sa[j][i], wo[j][i]), bs[j][i]);
                     }
+                    if (pre) {
+                        // t but for the mean's share, in the place of g_x
+                        const F2 pp = mul2(gh[j][i], wi[j][i]);
+                        gx[j][i] = fma2(pp, s1, gx[j][i]);
+                        if (post) {
+                            y[j][i] = add2(fb, y[j][i]);
+                            v1 = fma2(fb, y[j][i], v1);
+                        }
+                        v0 = fma2(pp, y[j][i], v0);
+                        dwi[j][i] = fma2(mul2(gh[j][i], y[j][i]), s1, dwi[j][i]);
+                    }
+                    if (post) v2 = fma2(fb, gx[j][i], v2);
                 }
             }
-            if (pre) {
-                const F2 m1(-(sum(v.sum()) * inv_m * sy * sy * sy));
-                release();
-                // t, the gradient of x_out in all, in the place of gx
-#pragma unroll
-                for (int j = 0; j < J; ++j)
-                    if (own[j])
-#pragma unroll
-                        for (int i = 0; i < H; ++i)
-                            gx[j][i] = fma2(m1, y[j][i], fma2(gh[j][i], mul2(s1, wi[j][i]), gx[j][i]));
-            }
-            v = F2(0.f);
+            float total[3] = {v0.sum(), v1.sum(), v2.sum()};
+            if constexpr (BWD) sum(total);
+            release();
+            const float m1 = total[0] * inv_m * sy * sy * sy;           // with t's factor s_y
+            const F2 n1(-m1), n2(-((total[2] - m1 * total[1]) * inv_m));
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 if (!own[j]) continue;
+                if (pre)
+#pragma unroll
+                    for (int i = 0; i < H; ++i) gx[j][i] = fma2(n1, y[j][i], gx[j][i]);
                 q[j].store(to(p.dx), gx[j]);
                 if (!post) continue;
                 F2 dg[H];
@@ -703,21 +692,10 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
                     const F2 tb = mul2(gx[j][i], bs[j][i]);
                     dwo[j][i] = fma2(sa[j][i], tb, dwo[j][i]);
                     if (gated) dg[i] = mul2(mul2(da[j][i], scale), mul2(wo[j][i], tb));
-                    gx[j][i] = mul2(gx[j][i], mul2(sa[j][i], wo[j][i]));          // q
-                    v = fma2(gx[j][i], bs[j][i], v);
+                    gx[j][i] = mul2(s0, fma2(mul2(sa[j][i], wo[j][i]), gx[j][i], mul2(bs[j][i], n2)));
                 }
                 if (gated) q[j].store(to(p.dgate), dg);
-            }
-            if (post) {
-                const F2 m2(-(sum(v.sum()) * inv_m));
-                if (!pre) release();
-#pragma unroll
-                for (int j = 0; j < J; ++j)
-                    if (own[j]) {
-#pragma unroll
-                        for (int i = 0; i < H; ++i) gx[j][i] = mul2(s0, fma2(bs[j][i], m2, gx[j][i]));
-                        q[j].store(to(p.db), gx[j]);
-                    }
+                q[j].store(to(p.db), gx[j]);
             }
         }
         if (++slot == s.slots) {
