@@ -228,8 +228,8 @@ int fill(Table<MAXT>& t, int n, const eqconv_tensor_t* ts, int from) {
     return i;
 }
 
-// Lists of up to 96 tensors fit the 4 KB of parameters that launch fastest.
-constexpr int kFew = 96, kMany = 1024;
+// Short lists launch with 1.2 KB of parameters, long ones with 30 KB.
+constexpr int kFew = 40, kMany = 1024;
 
 template <int MAXT>
 cudaError_t run(int n, const eqconv_tensor_t* ts, bool scale, float max_norm, float eps, float* norm, double* part,
