@@ -255,6 +255,9 @@ NORM = [  # N, L, C, dtype, gate
     (1501, 0, 3, "bf16", "none"),
     (301, 3, 210, "fp32", "silu"),
     (2, 0, 16384, "fp32", "sigmoid"),
+    (1400, 0, 264, "bf16", "silu"),          # many wide rows, from the narrowest
+    (1190, 0, 1032, "fp32", "sigmoid"),
+    (1184, 0, 4096, "fp16", "none"),
     (20011, 1, 8, "fp16", "sigmoid"),
 ]
 
