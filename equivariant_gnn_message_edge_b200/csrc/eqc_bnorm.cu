@@ -63,29 +63,22 @@ BnParams params_of(const BlockNormArgs& a) {
     return p;
 }
 
-// Channels a thread may move at once: 16 bytes, else 2, else 1, by C and the
-// tensors' starts.
-Shape shape_for(const BlockNormArgs& a) {
-    const int es = type_bytes(a.type);
-    uintptr_t all = 0;
-    for (const void* q : {a.x, a.b, a.gate, (const void*)a.x_out, (const void*)a.h, a.g_x, a.g_h,
-                          (const void*)a.dx, (const void*)a.db, (const void*)a.dgate})
-        all |= reinterpret_cast<uintptr_t>(q);
-    for (const int V : {16 / es, 2, 1})
-        if (a.C % V == 0 && all % (V * es) == 0) return shape_of(a.L, a.C, V);
-    return Shape{0, 0, 0, 0};
-}
-
-// The staged launch of these arguments (slots 0: none).
-Staged staged_for_args(const BlockNormArgs& a, bool bwd) {
-    uintptr_t all = 0;
+// The bytes that all tensors start on, 16 at most.
+int common_start(const BlockNormArgs& a) {
+    uintptr_t all = 16;
     for (const void* q : {a.x, a.b, a.gate, (const void*)a.x_out, (const void*)a.h, a.g_x, a.g_h,
                           (const void*)a.dx, (const void*)a.db, (const void*)a.dgate, (const void*)a.w_post,
                           (const void*)a.w_pre})
         all |= reinterpret_cast<uintptr_t>(q);
+    return (int)(all & (~all + 1));
+}
+
+// The staged launch of these arguments (slots 0: none).
+Staged staged_for_args(const BlockNormArgs& a, bool bwd) {
     const int tensors = bwd ? 2 * (a.g_h != nullptr) + (a.b != nullptr) + (a.g_x != nullptr) : 1 + (a.b != nullptr);
     if (!tensors) return Staged{};
-    return staged_shape(a.L, a.C, type_bytes(a.type), tensors, a.gate != nullptr, bwd, all % 16 == 0);
+    return staged_shape(a.L, a.C, type_bytes(a.type), tensors, a.gate != nullptr, bwd,
+                        common_start(a) == 16);
 }
 
 // rows: of the partial sums a CTA leaves (see bn_dw_reduce).
@@ -127,7 +120,7 @@ cudaError_t run(BnParams& p, const BlockNormArgs& a, bool bwd, cudaStream_t st, 
             default: return staged_f16(s, h, grid, bwd, st);
         }
     }
-    const Shape s = shape_for(a);
+    const Shape s = shape_of(a.L, a.C, type_bytes(a.type), bwd, common_start(a));
     *rows = 1;
     switch (a.type) {
         case EQCONV_F32: return run_f32(p, s, bwd, st);
@@ -147,13 +140,13 @@ cudaError_t block_norm_forward(const BlockNormArgs& a, cudaStream_t st) {
 }
 
 size_t block_norm_workspace(int L, int C, int N) {
-    // the most CTAs of any shape that C allows
-    int most = bn::cta_cap(bn::Shape{0, 0, 0, 0});
-    for (const int V : {8, 4, 2, 1}) {
-        if (C % V) continue;
-        const int k = bn::cta_cap(bn::shape_of(L, C, V));
-        if (k > most) most = k;
-    }
+    // the most CTAs of any shape that C and the tensors' starts allow
+    int most = bn::cta_cap(bn::Shape{0, 0, 0});
+    for (const int es : {2, 4})
+        for (const int pieces : {16, 8}) {
+            const int k = bn::cta_cap(bn::shape_of(L, C, es, true, pieces));
+            if (k > most) most = k;
+        }
     int64_t ctas = (int64_t)bn::kSMs * most;
     if (ctas > (int64_t)N * (L + 1)) ctas = (int64_t)N * (L + 1);
     // or, with the sums of all degrees, one CTA an SM, or several of wide nodes (64 threads at least)

@@ -45,7 +45,7 @@ struct BnParams {
     const void *g_x, *g_h;
     void *dx, *db, *dgate;
     float* part;         // [CTAs][2][C]: dw_post, dw_pre
-    int width;           // threads across the channels of a group (a power of two up to 32, or whole warps)
+    int width;           // staged kernels: threads across the channels of a node (a power of two up to 32, or whole warps)
 };
 
 // 2^x and 1/x by the hardware's approximations (2 and 1 units in the last
@@ -284,13 +284,12 @@ __global__ void __launch_bounds__(256) bn_bwd_stream(const BnParams p) {
 
 
 // ---------------------------------------------------------------------------
-// Resident kernels: a group's elements stay in registers between the sums.
-// A worker (p.width threads: part of a warp, a warp, or a whole CTA of warps)
-// owns a group; a thread owns V neighbouring channels (16 bytes where the rows
-// allow it), J times p.width V channels apart, in all K = 2l + 1 rows, of NB
-// nodes at a time.  Bound by memory: every tensor is moved once, and a worker
-// has all loads of its NB groups in flight together.  The weights and the sums
-// of their gradients stay in the thread that owns the channel for the whole
+// Resident kernels, for groups too large to be staged: a group's elements stay
+// in registers between the sums.  A CTA owns a group of one degree; a thread
+// owns V neighbouring channels, J times a CTA's width apart, in all K = 2l + 1
+// rows, of NB nodes at a time.  Bound by memory: every tensor is moved once,
+// all loads of a batch are in flight together.  The weights and the sums of
+// their gradients stay in the thread that owns the channel for the whole
 // persistent loop over nodes.
 
 // Sums of NB values over the worker's threads; every thread gets them.
@@ -331,18 +330,16 @@ template <class T, int V, int K, int J>
 __device__ __forceinline__ void fwd_groups(const BnParams& p, int l, float* red) {
     constexpr int NB = batch_of<V, K, J, false>();
     const int D = (p.L + 1) * (p.L + 1);
-    const int workers = p.width <= 32 ? (int)blockDim.x / p.width : 1;
-    const int worker = p.width <= 32 ? threadIdx.x / p.width : 0;
-    const int x0 = threadIdx.x - worker * p.width;
+    const int x0 = threadIdx.x, width = blockDim.x;
     const bool post = p.b != nullptr, pre = p.w_pre != nullptr, gated = p.gate != nullptr;
     const float inv_m = 1.f / ((float)K * (float)p.C);
-    const int64_t step = (int64_t)(p.first[l + 1] - p.first[l]) * workers * NB;
-    WorkerSum<NB> sum{red, p.width, 0};
+    const int64_t step = (int64_t)(p.first[l + 1] - p.first[l]) * NB;
+    WorkerSum<NB> sum{red, width, 0};
     Pack<float, V> wo[J], wi[J];
     bool own[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-        const int c = (x0 + j * p.width) * V;
+        const int c = (x0 + j * width) * V;
         own[j] = c < p.C;
         if (own[j] && post)
 #pragma unroll
@@ -351,11 +348,10 @@ __device__ __forceinline__ void fwd_groups(const BnParams& p, int l, float* red)
 #pragma unroll
             for (int e = 0; e < V; ++e) wi[j].e[e] = __ldg(p.w_pre + l * p.C + c + e);
     }
-    for (int64_t n0 = (int64_t)(blockIdx.x - p.first[l]) * workers * NB; n0 < p.N; n0 += step) {
+    for (int64_t nw = (int64_t)(blockIdx.x - p.first[l]) * NB; nw < p.N; nw += step) {
         Pack<T, V> x[NB][K][J], b[NB][K][J], g[NB][J];
-        const int64_t nw = n0 + worker * NB;
         const auto at = [&](int i, int m, int j) {
-            return ((nw + i) * D + l * l + m) * p.C + (x0 + j * p.width) * V;
+            return ((nw + i) * D + l * l + m) * p.C + (x0 + j * width) * V;
         };
 #pragma unroll
         for (int i = 0; i < NB; ++i)
@@ -368,7 +364,7 @@ __device__ __forceinline__ void fwd_groups(const BnParams& p, int l, float* red)
                     if (post) b[i][m][j].load(static_cast<const T*>(p.b) + at(i, m, j));
                 }
                 if (gated)
-                    g[i][j].load(static_cast<const T*>(p.gate) + ((nw + i) * (p.L + 1) + l) * p.C + (x0 + j * p.width) * V);
+                    g[i][j].load(static_cast<const T*>(p.gate) + ((nw + i) * (p.L + 1) + l) * p.C + (x0 + j * width) * V);
             }
         float sb[NB], sy[NB];
 #pragma unroll
@@ -449,22 +445,20 @@ __device__ __forceinline__ void fwd_groups(const BnParams& p, int l, float* red)
 }
 
 template <class T, int V, int K, int J>
-__device__ __forceinline__ void bwd_groups(const BnParams& p, int l, float* red, float* dw) {
+__device__ __forceinline__ void bwd_groups(const BnParams& p, int l, float* red) {
     constexpr int NB = batch_of<V, K, J, true>();
     const int D = (p.L + 1) * (p.L + 1);
-    const int workers = p.width <= 32 ? (int)blockDim.x / p.width : 1;
-    const int worker = p.width <= 32 ? threadIdx.x / p.width : 0;
-    const int x0 = threadIdx.x - worker * p.width;
+    const int x0 = threadIdx.x, width = blockDim.x;
     const bool post = p.b != nullptr, pre = p.g_h != nullptr, gated = p.gate != nullptr, more = p.g_x != nullptr;
     const float inv_m = 1.f / ((float)K * (float)p.C);
-    const int64_t step = (int64_t)(p.first[l + 1] - p.first[l]) * workers * NB;
-    WorkerSum<NB> sum{red, p.width, 0};
+    const int64_t step = (int64_t)(p.first[l + 1] - p.first[l]) * NB;
+    WorkerSum<NB> sum{red, width, 0};
     Pack<float, V> wo[J], wi[J];
     float dwo[J][V], dwi[J][V];
     bool own[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-        const int c = (x0 + j * p.width) * V;
+        const int c = (x0 + j * width) * V;
         own[j] = c < p.C;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
@@ -473,12 +467,11 @@ __device__ __forceinline__ void bwd_groups(const BnParams& p, int l, float* red,
             wi[j].e[e] = own[j] && pre ? __ldg(p.w_pre + l * p.C + c + e) : 0.f;
         }
     }
-    for (int64_t n0 = (int64_t)(blockIdx.x - p.first[l]) * workers * NB; n0 < p.N; n0 += step) {
+    for (int64_t nw = (int64_t)(blockIdx.x - p.first[l]) * NB; nw < p.N; nw += step) {
         Pack<T, V> x[NB][K][J], b[NB][K][J], gx[NB][K][J], gh[NB][K][J], g[NB][J];
         float sb[NB], sy[NB];
-        const int64_t nw = n0 + worker * NB;
         const auto at = [&](int i, int m, int j) {
-            return ((nw + i) * D + l * l + m) * p.C + (x0 + j * p.width) * V;
+            return ((nw + i) * D + l * l + m) * p.C + (x0 + j * width) * V;
         };
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
@@ -495,7 +488,7 @@ __device__ __forceinline__ void bwd_groups(const BnParams& p, int l, float* red,
                     if (pre) gh[i][m][j].load(static_cast<const T*>(p.g_h) + at(i, m, j));
                 }
                 if (gated)
-                    g[i][j].load(static_cast<const T*>(p.gate) + ((nw + i) * (p.L + 1) + l) * p.C + (x0 + j * p.width) * V);
+                    g[i][j].load(static_cast<const T*>(p.gate) + ((nw + i) * (p.L + 1) + l) * p.C + (x0 + j * width) * V);
             }
         }
         float sa[NB][J][V], da[NB][J][V];      // scale a(gate), scale a'(gate)
@@ -576,7 +569,7 @@ __device__ __forceinline__ void bwd_groups(const BnParams& p, int l, float* red,
                     o.set(e, da[i][j][e] * sb[i] * wo[j].e[e] * tb[e]);
                 }
                 if (gated)
-                    o.store(static_cast<T*>(p.dgate) + ((nw + i) * (p.L + 1) + l) * p.C + (x0 + j * p.width) * V);
+                    o.store(static_cast<T*>(p.dgate) + ((nw + i) * (p.L + 1) + l) * p.C + (x0 + j * width) * V);
             }
         if (!post) continue;
         sum(mqb);
@@ -597,33 +590,15 @@ __device__ __forceinline__ void bwd_groups(const BnParams& p, int l, float* red,
             }
         }
     }
-    // the CTA's sums: its workers' in order
     float* part = p.part + (int64_t)blockIdx.x * 2 * p.C;
-    if (workers == 1) {
 #pragma unroll
-        for (int j = 0; j < J; ++j)
-            if (own[j])
+    for (int j = 0; j < J; ++j)
+        if (own[j])
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    part[(x0 + j * p.width) * V + e] = dwo[j][e];
-                    part[p.C + (x0 + j * p.width) * V + e] = dwi[j][e];
-                }
-        return;
-    }
-    // several workers: width <= 32 and J = 1, at most 128 x V x 2 values
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-        dw[(threadIdx.x * 2) * V + e] = dwo[0][e];
-        dw[(threadIdx.x * 2 + 1) * V + e] = dwi[0][e];
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 2 * p.width * V; i += blockDim.x) {
-        const int which = i / (p.width * V), c = i - which * p.width * V;
-        if (c >= p.C) continue;
-        float s = 0.f;
-        for (int w = 0; w < workers; ++w) s += dw[((w * p.width + c / V) * 2 + which) * V + c % V];
-        part[which * p.C + c] = s;
-    }
+            for (int e = 0; e < V; ++e) {
+                part[(x0 + j * width) * V + e] = dwo[j][e];
+                part[p.C + (x0 + j * width) * V + e] = dwi[j][e];
+            }
 }
 
 // LMAX: the plan's L; J > 1 only for L = 0.  One CTA works on one degree.
@@ -643,51 +618,46 @@ template <class T, int V, int LMAX, int J>
 __global__ void __launch_bounds__(LMAX == 0 ? 512 : 256) bn_bwd_kernel(const BnParams p) {
     let_next_start();
     __shared__ float red[2 * 4 * 16];
-    __shared__ float dw[128 * 2 * V];
     const int l = degree_of(p, blockIdx.x);
-    if (l == 0) return bwd_groups<T, V, 1, J>(p, 0, red, dw);
+    if (l == 0) return bwd_groups<T, V, 1, J>(p, 0, red);
     if constexpr (LMAX >= 1)
-        if (l == 1) return bwd_groups<T, V, 3, 1>(p, 1, red, dw);
+        if (l == 1) return bwd_groups<T, V, 3, 1>(p, 1, red);
     if constexpr (LMAX >= 2)
-        if (l == 2) return bwd_groups<T, V, 5, 1>(p, 2, red, dw);
-    if constexpr (LMAX >= 3) return bwd_groups<T, V, 7, 1>(p, 3, red, dw);
+        if (l == 2) return bwd_groups<T, V, 5, 1>(p, 2, red);
+    if constexpr (LMAX >= 3) return bwd_groups<T, V, 7, 1>(p, 3, red);
 }
 
 // How a launch is cut: V channels a thread (0: the streaming kernels), J
-// times, `width` threads a group, `threads` a CTA.
+// times, `threads` a CTA.
 struct Shape {
-    int V, J, width, threads;
+    int V, J, threads;
 };
 
-// The widest vector that divides C and every pointer allows, then the fewest
-// channels a thread that fit: up to 512 threads x 4 vectors for L = 0, and
-// 256 threads x 1 for L > 0, whose groups hold up to 7 rows in registers.
-inline Shape shape_of(int L, int C, int V) {
-    Shape s{V, 1, 0, 0};
-    const int vecs = C / V, most = L == 0 ? 512 : 256;
-    while (s.J < (L == 0 ? 4 : 1) && (vecs + s.J - 1) / s.J > most) s.J *= 2;
-    const int across = (vecs + s.J - 1) / s.J;
-    if (across > most) return Shape{0, 0, 0, 0};
-    if (across > 32) {
-        s.width = s.threads = (across + 31) / 32 * 32;
-    } else {
-        s.width = 1;
-        while (s.width < across) s.width *= 2;
-        s.threads = 128;
+// Groups that fit a CTA's registers: 16 bytes a thread and row in one piece,
+// four for L = 0 (rows wider than the staged kernels take: up to 512 threads),
+// and for the fp32 backward at L = 3 also 8 bytes (rows of no whole 16 bytes of
+// which two nodes do not fit shared memory).  pieces: bytes all rows start on.
+inline Shape shape_of(int L, int C, int es, bool bwd, int pieces) {
+    Shape s{16 / es, L == 0 ? 4 : 1, 0};
+    if (pieces % 16 != 0 || C * es % 16 != 0) {
+        if (!(L == 3 && es == 4 && bwd && pieces % 8 == 0 && C % 2 == 0)) return Shape{0, 0, 0};
+        s.V = 2;
     }
+    const int across = (C / s.V + s.J - 1) / s.J;
+    if (across > (L == 0 ? 512 : 256) || (L == 1 && es == 4)) return Shape{0, 0, 0};
+    s.threads = (across + 31) / 32 * 32;
     return s;
 }
 
 // CTAs in proportion to the degrees' shares of the time, at least one each and
-// no more than there are batches of nodes.
-inline void split_ctas(BnParams& p, int most, int nodes_per_cta, const float (&share)[4]) {
-    const int64_t batches = ((int64_t)p.N + nodes_per_cta - 1) / nodes_per_cta;
+// no more than there are nodes.
+inline void split_ctas(BnParams& p, int most, const float (&share)[4]) {
     float all = 0.f;
     for (int l = 0; l <= p.L; ++l) all += share[l];
     p.first[0] = 0;
     for (int l = 0; l <= p.L; ++l) {
         int64_t k = (int64_t)(most * share[l] / all);
-        if (k > batches) k = batches;
+        if (k > p.N) k = p.N;
         if (k < 1) k = 1;
         p.first[l + 1] = p.first[l] + (int)k;
     }
@@ -715,26 +685,25 @@ cudaError_t launch(BnParams& p, const Shape& s, cudaStream_t st) {
     int resident = 65536 / (((regs + 7) / 8 * 8) * s.threads);
     resident = resident < 1 ? 1 : resident;
     const int cap = cta_cap(s);
-    p.width = s.width;
     // a batch of nodes takes its rows' time and about that of six rows more, waiting for its loads and sums
     constexpr int n0 = batch_of<V, 1, J, BWD>(), n1 = batch_of<V, 3, 1, BWD>(), n2 = batch_of<V, 5, 1, BWD>();
     const float share[4] = {1.f + 6.f / n0, 3.f + 6.f / n1, 5.f + 6.f / n2, 7.f + 6.f};
-    split_ctas(p, kSMs * (resident < cap ? resident : cap), s.width <= 32 ? s.threads / s.width : 1, share);
+    split_ctas(p, kSMs * (resident < cap ? resident : cap), share);
     kernel<<<p.first[p.L + 1], s.threads, 0, st>>>(p);
     count_launch();
     return cudaGetLastError();
 }
 
-template <class T, int V, bool BWD>
+template <class T, bool BWD>
 cudaError_t launch_for(BnParams& p, const Shape& s, cudaStream_t st) {
-    if (p.L == 0) {
-        if (s.J == 1) return launch<T, V, 0, 1, BWD>(p, s, st);
-        if (s.J == 2) return launch<T, V, 0, 2, BWD>(p, s, st);
-        return launch<T, V, 0, 4, BWD>(p, s, st);
-    }
-    if (p.L == 1) return launch<T, V, 1, 1, BWD>(p, s, st);
-    if (p.L == 2) return launch<T, V, 2, 1, BWD>(p, s, st);
-    return launch<T, V, 3, 1, BWD>(p, s, st);
+    constexpr int W = 16 / sizeof(T);
+    if (p.L == 0) return launch<T, W, 0, 4, BWD>(p, s, st);
+    if constexpr (W == 8)
+        if (p.L == 1) return launch<T, W, 1, 1, BWD>(p, s, st);
+    if (p.L == 2) return launch<T, W, 2, 1, BWD>(p, s, st);
+    if constexpr (W == 4 && BWD)
+        if (s.V == 2) return launch<T, 2, 3, 1, BWD>(p, s, st);
+    return launch<T, W, 3, 1, BWD>(p, s, st);
 }
 
 }  // namespace bn

@@ -7,12 +7,9 @@ namespace bn {
 
 cudaError_t EQC_BN_NAME(BnParams& p, const Shape& s, bool bwd, cudaStream_t st) {
     using T = EQC_BN_TYPE;
-    constexpr int kWide = 16 / sizeof(T);
-    if (s.V == kWide) return bwd ? launch_for<T, kWide, true>(p, s, st) : launch_for<T, kWide, false>(p, s, st);
-    if (s.V == 2) return bwd ? launch_for<T, 2, true>(p, s, st) : launch_for<T, 2, false>(p, s, st);
-    if (s.V == 1) return bwd ? launch_for<T, 1, true>(p, s, st) : launch_for<T, 1, false>(p, s, st);
+    if (s.V) return bwd ? launch_for<T, true>(p, s, st) : launch_for<T, false>(p, s, st);
     const float rows[4] = {1.f, 3.f, 5.f, 7.f};
-    split_ctas(p, kStreamCtas, 1, rows);
+    split_ctas(p, kStreamCtas, rows);
     if (bwd) {
         const int smem = 2 * p.C * (int)sizeof(float);
         if (smem > 40 * 1024) {

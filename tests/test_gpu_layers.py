@@ -255,6 +255,13 @@ NORM = [  # N, L, C, dtype, gate
     (1501, 0, 3, "bf16", "none"),
     (301, 3, 210, "fp32", "silu"),
     (2, 0, 16384, "fp32", "sigmoid"),
+    (40, 3, 502, "fp32", "tanh"),            # two nodes do not fit shared memory backward
+    (40, 3, 700, "fp32", "silu"),
+    (25, 1, 1500, "bf16", "sigmoid"),
+    (25, 2, 900, "fp32", "none"),
+    (30, 0, 6000, "fp32", "tanh"),
+    (20, 0, 9000, "fp32", "silu"),           # too wide for registers too
+    (20, 1, 1999, "fp16", "sigmoid"),
     (1400, 0, 264, "bf16", "silu"),          # many wide rows, from the narrowest
     (1190, 0, 1032, "fp32", "sigmoid"),
     (1184, 0, 4096, "fp16", "none"),
