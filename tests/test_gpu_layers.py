@@ -673,6 +673,37 @@ def test_own_stream_and_graph_replay(N, L, C, V):
         assert all(torch.equal(a, c) for a, c in zip(r, want))
 
 
+def test_captured_autograd_step():
+    """Forward and backward through autograd in one captured graph: a replay
+    gives the gradients of the inputs' current contents."""
+    N, L, C, V = 500, 1, 48, 30
+    emb, norm = layers.Embedding(V, C), layers.BlockNorm(natural_irreps(L), C)
+    z, table, _ = _embed_case(N, V, C, "fp32", "fp32", "int32")
+    x, b, gate, wo, wi, gx, gh = _norm_case(N, L, C, "fp32", "sigmoid")
+    leaves = [t.requires_grad_(True) for t in (table, b, gate, wo, wi)]
+
+    def step():
+        x0 = torch.cat([emb(z, table, 1.5)[:, None], x[:, 1:]], 1)
+        xo, h = norm(x0, b, gate, wo, wi, 0.7)
+        return torch.autograd.grad((xo * gx).sum() + (h * gh).sum(), leaves)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    with torch.no_grad():
+        for t in leaves:
+            t.mul_(1.25)
+    g.replay()
+    torch.cuda.synchronize()
+    for a, c in zip(got, step()):
+        assert torch.equal(a, c)
+
+
 def test_two_streams_at_once():
     """Calls of one operator that overlap on two streams do not disturb each other."""
     V, C, L = 5000, 64, 1
