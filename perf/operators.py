@@ -260,15 +260,17 @@ def _op(c):
 
 def _own(st):
     c = st["case"]
+    if c["op"] != "clip" and "handle" not in st:
+        st["handle"] = _op(c)          # found once: a program holds its layer and does not look it up at every call
     if c["op"] == "embed":
-        return _op(c).forward_raw(st["ids"], st["table"], c["scale"])
+        return st["handle"].forward_raw(st["ids"], st["table"], c["scale"])
     if c["op"] == "embed_grad":
-        return _op(c).backward_raw(st["ids"], st["gy"], c["scale"])
+        return st["handle"].backward_raw(st["ids"], st["gy"], c["scale"])
     if c["op"] == "clip":
         from equivariant_gnn_message_edge_b200 import layers
         norm = layers.clip_gradients(st["grads"], st["bound"], out=st["out"])
         return dict(norm=norm, grads=st["out"])
-    op = _op(c)
+    op = st["handle"]
     args = st["x"], st["b"], st["gate"], st["w_post"], st["w_pre"]
     x, h, stats = op.forward_raw(*args, scale=c["scale"], save=c["train"])
     out = dict(x=x) if c["post"] else {}
