@@ -143,7 +143,7 @@ __device__ __forceinline__ int block_exclusive(int v, int* warp_sums) {
     return before + inc - v;
 }
 
-// Sort of up to 8 x 8192 nodes in one launch by one cluster: keys and node
+// Sort of up to 8 x 8192 nodes (sort_few) in one launch by one cluster: keys and node
 // numbers stay in the CTAs' shared memory between passes and are scattered
 // into each other's over the cluster (least significant digit first).  Bound
 // by latency; the launch it saves per step is worth more than its idle SMs.
@@ -360,8 +360,8 @@ __global__ void __launch_bounds__(kLsdThreads) embed_scatter_kernel(const void* 
 }
 
 // Rows of a block that writes zeros: 512 KB of them, so that the search takes
-// little of its time, and at most 2048.
-constexpr int kZeroRows = 2048, kZeroBytes = 512 * 1024;
+// little of its time, and at most one a thread.
+constexpr int kZeroRows = 256, kZeroBytes = 512 * 1024;
 constexpr int64_t kSortZeroBytes = 64 << 20;
 
 struct SumParams {
@@ -395,9 +395,9 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const SumParams p, const
         __shared__ bool empty[kZeroRows];
         const int64_t v0 = p.zero_from + (int64_t)(blockIdx.x - p.sum_blocks) * p.zero_rows;
         const int rows = (int)(p.V - v0 < p.zero_rows ? p.V - v0 : p.zero_rows);
-        for (int r = threadIdx.x; r < rows; r += 256) {
-            const int v = (int)(v0 + r), at = lower_bound(p.keys, p.N, v);
-            empty[r] = at >= p.N || p.keys[at] != v;
+        if ((int)threadIdx.x < rows) {
+            const int v = (int)(v0 + threadIdx.x), at = lower_bound(p.keys, p.N, v);
+            empty[threadIdx.x] = at >= p.N || p.keys[at] != v;
         }
         __syncthreads();
         Pack<T, VE> zero;
@@ -483,57 +483,93 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const SumParams p, const
 }
 
 // Types that reach over tile ends: the tile in which such a type begins adds
-// its partial row and those of the tiles behind it, shares of them by worker
-// and the workers' sums in order.
+// its partial row and those of the tiles behind it, in tile order.  A worker
+// (1 << lx_log2 lanes, one tile and slab) does that alone where the type ends
+// within kAlone tiles; what is longer is done by the block together, shares of
+// the tiles by worker and the workers' sums in order.
+constexpr int kAlone = 8;
+
 template <class T, int VE>
 __global__ void __launch_bounds__(256) embed_join_kernel(const SumParams p, T* dtable) {
     wait_for_last();
-    const int tile = blockIdx.x, slab = blockIdx.y;
-    const int64_t end = (int64_t)(tile + 1) * p.R;       // < N for every tile of the grid
-    const int k = __ldg(p.keys + end - 1);
-    if (k == (int)p.V || __ldg(p.keys + end) != k) return;
-    if (tile > 0 && __ldg(p.keys + end - p.R - 1) == k) return;      // begun in an earlier tile
-    // tile of the type's last node: the tiles behind that begin with the type follow one another
-    int last = tile;
-    for (int more = 256; more == 256; last += more) {
-        const int64_t at = (int64_t)(last + 1 + threadIdx.x) * p.R;
-        more = __syncthreads_count(at < p.N && __ldg(p.keys + at) == k);
-    }
+    __shared__ float sums[256 * VE];
+    __shared__ int long_type[256];         // of each worker: the type that takes the whole block, or V
     const int lanes = 1 << p.lx_log2, workers = 256 >> p.lx_log2;
     const int x = threadIdx.x & (lanes - 1), w = threadIdx.x >> p.lx_log2;
-    const int c = ((slab << p.lx_log2) + x) * VE;
-    const int share = (last - tile + workers - 1) / workers;          // of the tiles behind the first
-    const int t0 = tile + 1 + w * share, t1 = t0 + share < last + 1 ? t0 + share : last + 1;
-    __shared__ float sums[256 * VE];
-    float acc[VE];
+    const unsigned worker0 = blockIdx.x * (unsigned)workers;
+    // of a worker: its tile (a block's tiles follow one another: one of them at most begins a long type, or few), its
+    // channels, and the type that begins in the tile and goes on behind it (V: none)
+    const unsigned tiles = p.tiles - 1;
+    const auto tile_of = [&](unsigned worker) { return (int)(worker % tiles); };
+    const auto channel_of = [&](unsigned worker) { return (((int)(worker / tiles) << p.lx_log2) + x) * VE; };
+    const auto type_of = [&](int tile) {
+        const int64_t end = (int64_t)(tile + 1) * p.R;
+        const int k = __ldg(p.keys + end - 1), next = __ldg(p.keys + end);
+        const bool before = tile > 0 && __ldg(p.keys + end - p.R - 1) == k;
+        return next == k && !before ? k : (int)p.V;
+    };
+    const auto starts = [&](int64_t t, int k) { return t * p.R < p.N && __ldg(p.keys + t * p.R) == k; };
+    const auto add = [&](float (&acc)[VE], int64_t row, int c) {
+        Pack<float, VE> v;
+        v.load(p.part + row * p.C + c);
 #pragma unroll
-    for (int e = 0; e < VE; ++e) acc[e] = 0.f;
-    if (c < p.C) {
-        if (w == 0) {
-            Pack<float, VE> v;
-            v.load(p.part + ((int64_t)tile * 2 + 1) * p.C + c);
+        for (int e = 0; e < VE; ++e) acc[e] += v.e[e];
+    };
+    const auto finish = [&](const float (&acc)[VE], int k, int c) {
+        Pack<T, VE> out;
 #pragma unroll
-            for (int e = 0; e < VE; ++e) acc[e] = v.e[e];
+        for (int e = 0; e < VE; ++e) out.set(e, acc[e] * p.scale);
+        out.store(dtable + (int64_t)k * p.C + c);
+    };
+    {
+        const int tile = tile_of(worker0 + w), c = channel_of(worker0 + w);
+        const int k = worker0 + w < tiles * p.slabs ? type_of(tile) : (int)p.V;
+        int behind = 0;      // tiles behind the first, kAlone + 1: more
+        if (k != (int)p.V) {
+#pragma unroll
+            for (int i = 1; i <= kAlone + 1; ++i) behind += starts(tile + i, k);
+            if (behind <= kAlone && c < p.C) {
+                float acc[VE];
+#pragma unroll
+                for (int e = 0; e < VE; ++e) acc[e] = 0.f;
+                add(acc, (int64_t)tile * 2 + 1, c);
+#pragma unroll
+                for (int i = 1; i <= kAlone; ++i)
+                    if (i <= behind) add(acc, (int64_t)(tile + i) * 2, c);
+                finish(acc, k, c);
+            }
         }
-#pragma unroll 8
-        for (int t = t0; t < t1; ++t) {
-            Pack<float, VE> v;
-            v.load(p.part + (int64_t)t * 2 * p.C + c);
-#pragma unroll
-            for (int e = 0; e < VE; ++e) acc[e] += v.e[e];
-        }
+        if (x == 0) long_type[w] = behind > kAlone ? k : (int)p.V;
     }
-#pragma unroll
-    for (int e = 0; e < VE; ++e) sums[threadIdx.x * VE + e] = acc[e];
     __syncthreads();
-    if (w != 0 || c >= p.C) return;
-    for (int o = 1; o < workers; ++o)
+    for (int u = 0; u < workers; ++u) {
+        const int k = long_type[u];
+        if (k == (int)p.V) continue;
+        const int tile = tile_of(worker0 + u), c = channel_of(worker0 + u);
+        // tile of the type's last node: the tiles behind that begin with the type follow one another
+        int last = tile;
+        for (int more = 256; more == 256; last += more) more = __syncthreads_count(starts((int64_t)last + 1 + threadIdx.x, k));
+        const int share = (last - tile + workers - 1) / workers;          // of the tiles behind the first
+        const int t0 = tile + 1 + w * share, t1 = t0 + share < last + 1 ? t0 + share : last + 1;
+        float acc[VE];
 #pragma unroll
-        for (int e = 0; e < VE; ++e) acc[e] += sums[((o << p.lx_log2) + x) * VE + e];
-    Pack<T, VE> out;
+        for (int e = 0; e < VE; ++e) acc[e] = 0.f;
+        if (c < p.C) {
+            if (w == 0) add(acc, (int64_t)tile * 2 + 1, c);
+#pragma unroll 8
+            for (int t = t0; t < t1; ++t) add(acc, (int64_t)t * 2, c);
+        }
 #pragma unroll
-    for (int e = 0; e < VE; ++e) out.set(e, acc[e] * p.scale);
-    out.store(dtable + (int64_t)k * p.C + c);
+        for (int e = 0; e < VE; ++e) sums[threadIdx.x * VE + e] = acc[e];
+        __syncthreads();
+        if (w == 0 && c < p.C) {
+            for (int o = 1; o < workers; ++o)
+#pragma unroll
+                for (int e = 0; e < VE; ++e) acc[e] += sums[((o << p.lx_log2) + x) * VE + e];
+            finish(acc, k, c);
+        }
+        __syncthreads();
+    }
 }
 
 // Few nodes and a small table: one launch without a sort.  A CTA owns a type
@@ -663,17 +699,25 @@ int bit_length(int64_t v) {
     return b;
 }
 
+int sort_passes(int64_t V) { return cdiv(bit_length(V), kDigitBits); }
+
+// Whether one cluster sorts: up to 65536 nodes in one pass; where there are
+// more passes (V of 512 and more) up to 16384, its eight SMs being slower than
+// all of them in three launches a pass (60000 nodes, 20000 types: 36 us in one
+// cluster, 22 us in tiles; 16384 nodes, 65536 types: 18 and 20 us).
+bool sort_few(int64_t V, int64_t N) { return N <= (sort_passes(V) == 1 ? kMaxCluster * kSortCap : 16384); }
+
 struct EmbedWs {
     size_t keys, perm, keys2, perm2, hist, total, part, bytes;
 };
 // Space for any of the vector widths (the widest tiles come with width 1).
-EmbedWs embed_layout(int C, int64_t N) {
+EmbedWs embed_layout(int64_t V, int C, int64_t N) {
     const auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
     EmbedWs w{};
     size_t o = 0;
     w.keys = o; o += up(4 * (size_t)N);
     w.perm = o; o += up(4 * (size_t)N);
-    if (N > (int64_t)kMaxCluster * kSortCap) {
+    if (!sort_few(V, N)) {
         const size_t tiles = cdiv(N, kLsdTile);
         w.keys2 = o; o += up(4 * (size_t)N);
         w.perm2 = o; o += up(4 * (size_t)N);
@@ -775,7 +819,7 @@ cudaError_t sort_in_tiles(const EmbedArgs& a, int digit_bits, int passes, char* 
 // 6.9 us in one launch, 14.5 us in three.
 static bool embed_few(int64_t V, int C, int64_t N) { return N <= 4096 && V * cdiv(C, 32) <= 2 * 148; }
 
-size_t embed_workspace(int64_t V, int C, int64_t N) { return N == 0 || embed_few(V, C, N) ? 0 : embed_layout(C, N).bytes; }
+size_t embed_workspace(int64_t V, int C, int64_t N) { return N == 0 || embed_few(V, C, N) ? 0 : embed_layout(V, C, N).bytes; }
 
 cudaError_t embed_backward(const EmbedArgs& a, const void* gy, int64_t gy_stride, void* dtable, void* ws,
                            cudaStream_t st) {
@@ -802,18 +846,18 @@ cudaError_t embed_backward(const EmbedArgs& a, const void* gy, int64_t gy_stride
                 });
             });
         });
-    const EmbedWs w = embed_layout(a.C, a.N);
+    const EmbedWs w = embed_layout(a.V, a.C, a.N);
     char* base = static_cast<char*>(ws);
     int* keys = reinterpret_cast<int*>(base + w.keys);
     int* perm = reinterpret_cast<int*>(base + w.perm);
     // keys 0..V in equal digits of at most 9 bits
-    const int bits = bit_length(a.V), passes = cdiv(bits, kDigitBits), digit_bits = cdiv(bits, passes);
+    const int bits = bit_length(a.V), passes = sort_passes(a.V), digit_bits = cdiv(bits, passes);
     cudaError_t err;
     // A sort of one cluster leaves the other SMs idle for some 10 us: they write zeros to the first rows meanwhile
     // (whole 16 bytes, up to 64 MB), and the sums overwrite those that have nodes.
     int64_t zero_to = 0;
     const int64_t row = (int64_t)a.C * type_bytes(a.in_type);
-    if (a.N <= (int64_t)kMaxCluster * kSortCap) {
+    if (sort_few(a.V, a.N)) {
         if (reinterpret_cast<uintptr_t>(dtable) % 16 == 0) {
             zero_to = kSortZeroBytes / row;
             zero_to = (zero_to < a.V ? zero_to : a.V) / 16 * 16;
@@ -854,7 +898,8 @@ cudaError_t embed_backward(const EmbedArgs& a, const void* gy, int64_t gy_stride
                                              256, st, p, static_cast<const O*>(gy), static_cast<T*>(dtable));
                 count_launch();
                 if (e == cudaSuccess && s.tiles > 1) {
-                    e = launch_after(embed_join_kernel<T, VE>, dim3(s.tiles - 1, s.slabs), 256, st, p,
+                    e = launch_after(embed_join_kernel<T, VE>,
+                                     cdiv(((int64_t)(s.tiles - 1) * s.slabs) << s.lx_log2, 256), 256, st, p,
                                      static_cast<T*>(dtable));
                     count_launch();
                 }

@@ -64,6 +64,10 @@ EMBED = [  # N, V, C, table, out, ids
     (4096, 297, 32, "fp16", "fp16", "int32"),
     (65536, 40, 4, "fp32", "fp32", "int64"),           # the largest one-cluster sort, and just over
     (65537, 600, 4, "bf16", "bf16", "int32"),
+    (16384, 600, 8, "fp32", "bf16", "int64"),          # the same for two passes
+    (16385, 70000, 8, "fp32", "fp32", "int32"),
+    (30000, 3000, 36, "fp32", "fp32", "int64"),        # types of about a tile
+    (9000, 40, 520, "fp16", "fp16", "int32"),          # types of many tiles, several slabs
 ]
 
 
