@@ -77,7 +77,7 @@ int common_start(const BlockNormArgs& a) {
 Staged staged_for_args(const BlockNormArgs& a, bool bwd) {
     const int tensors = bwd ? 2 * (a.g_h != nullptr) + (a.b != nullptr) + (a.g_x != nullptr) : 1 + (a.b != nullptr);
     if (!tensors) return Staged{};
-    return staged_shape(a.L, a.C, type_bytes(a.type), tensors, a.gate != nullptr, bwd,
+    return staged_shape(a.N, a.L, a.C, type_bytes(a.type), tensors, a.gate != nullptr, bwd,
                         common_start(a) == 16);
 }
 
@@ -90,6 +90,7 @@ cudaError_t run(BnParams& p, const BlockNormArgs& a, bool bwd, cudaStream_t st, 
         p.width = h.width;
         s.slots = h.slots;
         s.nodes = h.nodes;
+        s.batch = h.batch;
         s.ring = h.ring;
         s.total = ((int64_t)a.N + h.nodes - 1) / h.nodes;
         int o = 0;

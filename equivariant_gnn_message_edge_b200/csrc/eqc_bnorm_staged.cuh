@@ -9,7 +9,7 @@
 // and a thread's channels are then `width` apart instead of neighbours, so that
 // every element is read alone and a warp's lanes still lie side by side.
 //
-// A worker is a warp (32 / width nodes a slot, each warp with slots of its own)
+// A worker is a warp (32 / width nodes at a time, each warp with slots of its own)
 // or, for wide nodes, the whole CTA (one node a slot).  Its threads own V
 // channels of every row of the node.
 #pragma once
@@ -25,6 +25,7 @@ constexpr int kMaxSlots = 16;
 struct StagedParams {
     BnParams p;
     int slots, nodes;          // slots of the ring, nodes a slot
+    int batch;                 // of which a worker takes nodes / batch at a time
     int64_t total;             // slots' worth of nodes in all
     // the tensors of a slot: where they come from, their bytes a node, their place in the slot
     int tensors;
@@ -394,8 +395,9 @@ __global__ void __launch_bounds__(CTA ? 256 : BWD ? 256 : 512, 1) bn_staged_kern
     bool ok = true;
     // a node's statistics are fetched while the worker's last node is worked on
     float sb_next[BWD ? L + 1 : 1], sy_next[BWD ? L + 1 : 1];
-    const auto fetch = [&](int k) {
-        const int64_t n = (blockIdx.x + (int64_t)k * gridDim.x) * s.nodes + sub;
+    const int each = CTA ? 1 : 32 / width;       // nodes a worker takes at a time
+    const auto first_of = [&](int k) { return (blockIdx.x + (int64_t)k * gridDim.x) * s.nodes + sub; };
+    const auto fetch = [&](int64_t n) {
 #pragma unroll
         for (int l = 0; l < (BWD ? L + 1 : 1); ++l) {
             sb_next[l] = n < p.N && p.b ? __ldg(p.stats + n * (L + 1) + l) : 0.f;
@@ -403,17 +405,9 @@ __global__ void __launch_bounds__(CTA ? 256 : BWD ? 256 : 512, 1) bn_staged_kern
         }
     };
     if constexpr (BWD)
-        if (worker < mine) fetch(worker);
+        if (worker < mine) fetch(first_of(worker));
     for (int k = worker; k < mine; k += workers) {
         const int slot = k % s.slots;
-        const int64_t n = (blockIdx.x + (int64_t)k * gridDim.x) * s.nodes + sub;
-        const bool live = n < p.N;
-        float sb[L + 1], sy[L + 1];
-        if constexpr (BWD) {
-#pragma unroll
-            for (int l = 0; l <= L; ++l) sb[l] = sb_next[l], sy[l] = sy_next[l];
-            fetch(k + workers);
-        }
         if (!bulk::wait(full + slot, (uint32_t)(k / s.slots) & 1u)) {
             atomicOr(s.status, 4u);
             ok = false;
@@ -427,14 +421,28 @@ __global__ void __launch_bounds__(CTA ? 256 : BWD ? 256 : 512, 1) bn_staged_kern
         const unsigned char* base = ring.base + (int64_t)slot * s.slot_bytes;
         const auto at = [&](int t) {
             const uint32_t lead = APART ? lead_of(s, t, blockIdx.x + (int64_t)k * gridDim.x) : 0;
-            return reinterpret_cast<const T*>(base + s.offset[t] + lead + sub * s.bytes[t]);
+            return base + s.offset[t] + lead;
         };
-        const View<T> v{at(s.i_x), at(s.i_b), at(s.i_gx), at(s.i_gh), at(s.i_g)};
-        const int64_t row = n * D * p.C, grow = n * (L + 1) * p.C;
-        if constexpr (BWD)
-            bwd_node<T, V, L, APART>(p, v, w, q, own, live, row, grow, sb, sy, dwo, dwi, sum);
-        else
-            fwd_node<T, V, L, APART>(p, v, w, q, own, live, row, n * (L + 1), x0 == 0, sum);
+        const unsigned char *xs = at(s.i_x), *bs = at(s.i_b), *gxs = at(s.i_gx), *ghs = at(s.i_gh), *gs = at(s.i_g);
+        const int batch = L == 0 && !CTA ? s.batch : 1;
+        for (int m = 0; m < batch; ++m) {
+            const int64_t n = first_of(k) + m * each;
+            if (n - sub >= p.N) break;           // for all lanes alike
+            const bool live = n < p.N;
+            const int node = (m * each + sub) * D * p.C, group = (m * each + sub) * (L + 1) * p.C;
+            const auto of = [&](const unsigned char* q, int i) { return reinterpret_cast<const T*>(q) + i; };
+            const View<T> v{of(xs, node), of(bs, node), of(gxs, node), of(ghs, node), of(gs, group)};
+            const int64_t row = n * D * p.C, grow = n * (L + 1) * p.C;
+            if constexpr (BWD) {
+                float sb[L + 1], sy[L + 1];
+#pragma unroll
+                for (int l = 0; l <= L; ++l) sb[l] = sb_next[l], sy[l] = sy_next[l];
+                fetch(m + 1 < batch ? n + each : first_of(k + workers));
+                bwd_node<T, V, L, APART>(p, v, w, q, own, live, row, grow, sb, sy, dwo, dwi, sum);
+            } else {
+                fwd_node<T, V, L, APART>(p, v, w, q, own, live, row, n * (L + 1), x0 == 0, sum);
+            }
+        }
         // everyone has read the slot: its next copies may come
         if constexpr (CTA) __syncthreads();
         else __syncwarp();
@@ -719,7 +727,7 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
 
 // How a staged launch is cut; slots 0: not staged.
 struct Staged {
-    int V, J, width, threads, slots, nodes, ctas, smem, ring;
+    int V, J, width, threads, slots, nodes, batch, ctas, smem, ring;
     bool row;          // the kernel for wide rows
     bool apart;        // a thread's channels are `width` apart
 };
@@ -729,10 +737,11 @@ inline int64_t part_bytes(int64_t bytes, bool apart) { return apart ? (bytes + 3
 
 // Two slots an SM at least, of what its shared memory holds.  tensors: as large
 // as x; gated: the gate too; aligned: all start on 16 bytes.
-inline Staged staged_shape(int L, int C, int es, int tensors, bool gated, bool bwd, bool aligned) {
+inline Staged staged_shape(int64_t N, int L, int C, int es, int tensors, bool gated, bool bwd, bool aligned) {
     Staged s{};
     const int room = 224 * 1024, wbytes = (2 * (L + 1) * C * 4 + 15) / 16 * 16;
     s.apart = !aligned || C * es % 16 != 0;
+    s.batch = 1;
     s.V = L == 0 ? 16 / es : 4;
     s.J = 1;
     const int vecs = (C + s.V - 1) / s.V;
@@ -743,9 +752,15 @@ inline Staged staged_shape(int L, int C, int es, int tensors, bool gated, bool b
     if (vecs <= 32) {
         s.width = 1;
         while (s.width < vecs) s.width *= 2;
-        s.nodes = 32 / s.width;
         s.ctas = 1;
         s.ring = wbytes;
+        // rows (L = 0) are small: so many a slot that the slots of all warps fill the shared memory, while there are
+        // rows for all (131072 fp32 rows of 128: forward 120 -> 81 us, backward 182 -> 138 us)
+        const int most = bwd ? 8 : 16, each = 32 / s.width;
+        const int64_t full = (room - wbytes) / most / slot(each), some = N / ((int64_t)148 * most * each);
+        s.batch = (int)(full < some ? full : some);
+        s.batch = L > 0 || s.batch < 1 ? 1 : s.batch > 16 ? 16 : s.batch;
+        s.nodes = each * s.batch;
         const int64_t fit = (room - wbytes) / slot(s.nodes);
         s.slots = (int)(fit < kMaxSlots ? fit : kMaxSlots);
         if (s.slots < 2) return Staged{};
@@ -754,7 +769,7 @@ inline Staged staged_shape(int L, int C, int es, int tensors, bool gated, bool b
         // show the parity of the phase it wants.
         // One slot a warp is best where that gives no more than 8 warps backward (222 registers a thread; lmax2: 8
         // slots of 8 warps 170 us, 10 of 5 warps 219 us) or 16 forward (108 us; 16 slots of 8 warps 109 us).
-        const int most = bwd ? 8 : 16, warps = s.slots < most ? s.slots : most;
+        const int warps = s.slots < most ? s.slots : most;
         s.slots = s.slots / warps * warps;
         s.threads = 32 * warps;
         // the reduction of the weight gradients takes threads * V floats of the ring
