@@ -742,7 +742,7 @@ inline Staged staged_shape(int64_t N, int L, int C, int es, int tensors, bool ga
     const int room = 224 * 1024, wbytes = (2 * (L + 1) * C * 4 + 15) / 16 * 16;
     s.apart = !aligned || C * es % 16 != 0;
     s.batch = 1;
-    s.V = L == 0 ? 16 / es : 4;
+    s.V = L == 0 || (L <= 2 && !s.apart) ? 16 / es : 4;
     s.J = 1;
     const int vecs = (C + s.V - 1) / s.V;
     const auto slot = [&](int nodes) {
@@ -837,7 +837,7 @@ cudaError_t launch_row(const StagedParams& s, const Staged& h, int grid, cudaStr
 
 template <class T, bool BWD, bool APART>
 cudaError_t staged_for(const StagedParams& s, const Staged& h, int grid, cudaStream_t st) {
-    constexpr int W = 16 / sizeof(T);
+    constexpr int W = 16 / sizeof(T), V = APART ? 4 : W;
     const bool cta = h.width > 32;
     if (h.row) {
         if constexpr (W == 8)
@@ -848,11 +848,11 @@ cudaError_t staged_for(const StagedParams& s, const Staged& h, int grid, cudaStr
         case 0:
             return launch_staged<T, W, 0, BWD, false, APART>(s, h, grid, st);
         case 1:
-            return cta ? launch_staged<T, 4, 1, BWD, true, APART>(s, h, grid, st)
-                       : launch_staged<T, 4, 1, BWD, false, APART>(s, h, grid, st);
+            return cta ? launch_staged<T, V, 1, BWD, true, APART>(s, h, grid, st)
+                       : launch_staged<T, V, 1, BWD, false, APART>(s, h, grid, st);
         case 2:
-            return cta ? launch_staged<T, 4, 2, BWD, true, APART>(s, h, grid, st)
-                       : launch_staged<T, 4, 2, BWD, false, APART>(s, h, grid, st);
+            return cta ? launch_staged<T, V, 2, BWD, true, APART>(s, h, grid, st)
+                       : launch_staged<T, V, 2, BWD, false, APART>(s, h, grid, st);
         default:
             return cta ? launch_staged<T, 4, 3, BWD, true, APART>(s, h, grid, st)
                        : launch_staged<T, 4, 3, BWD, false, APART>(s, h, grid, st);
