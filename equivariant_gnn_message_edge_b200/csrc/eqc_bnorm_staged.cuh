@@ -12,6 +12,10 @@
 // A worker is a warp (32 / width nodes at a time, each warp with slots of its own)
 // or, for wide nodes, the whole CTA (one node a slot).  Its threads own V
 // channels of every row of the node.
+//
+// Bound by memory for fp32 (32768 lmax2 nodes of 128 channels: forward 107 us,
+// 6.1 TB/s; backward 167 us, 6.0 TB/s), by instructions for 16-bit elements
+// (the same nodes in bf16: 59 and 138 us).
 #pragma once
 
 #include "eqc_bnorm.cuh"

@@ -2,9 +2,11 @@
 //   n = sqrt(sum over all tensors and elements of g^2)
 //   k = min(1, max_norm / (n + eps))       g <- k g
 // Bound by memory: every element read once for the norm, and read and written
-// once for the scaling.  Squares are summed in fp64 (16 bytes of 43 GB/s per SM
-// leave the fp64 units mostly idle), so no gradient is so large or so small
-// that its square leaves the range, and the order of the sums is fixed.
+// once for the scaling.  Squares are summed in fp64 (at the memory's rate an SM
+// has some 6 fp32 elements a clock to add, a tenth of what its fp64 units do),
+// so no gradient is so large or so small that its square leaves the range, and
+// the order of the sums is fixed.  564 MB of bf16 with some fp32: norm 102 us
+// (5.5 TB/s), scaling 178 us (6.3 TB/s, a part of the reads from L2).
 #include <cuda_runtime.h>
 
 #include <cmath>

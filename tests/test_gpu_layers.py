@@ -295,6 +295,10 @@ def _norm_tols(args, gx, gh, scale, eps, kind, dtype):
     x, b, gate, wo, wi = (np64(t) for t in args)
     L, C = int(round(x.shape[1] ** 0.5)) - 1, x.shape[2]
     r = _rms_err(L, C) + 12 * U                    # a product of up to a dozen rounded factors with 1/rms
+    if kind == "tanh" and dtype != torch.float32:
+        # (1 - q) / (1 + q) with q = exp(-2|g|): 1 - q >= 2|g| (1 - |g|) is off by about 2^-24, and 16-bit gates take
+        # that form down to |g| = 2^-8, where it is 2^-24 / 2^-7 of the value; below, g itself is g^2 / 3 < 2^-17 off
+        r += 2.0 ** -17
     ab = lambda v: None if v is None else np.abs(v)  # noqa: E731
     y, h = ol.block_norm(x, b, gate, wo, wi, scale, eps, kind)
     amp = y if y is not None else x
