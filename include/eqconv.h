@@ -469,7 +469,8 @@ EQCONV_API int eqconv_embedding_plan_create(eqconv_plan_t* out, int64_t n_types,
 
 /* y as above; one launch on `stream`.  ids are int32 or int64 (id_bits 32 or
  * 64).  Rows of T and y start table_stride and y_stride elements apart (>= C).
- * ids out of range set the status word (bit 1); their rows of y are 0. */
+ * ids out of range set the status word (bit 1); their rows of y are 0.  y
+ * overlaps neither T nor ids. */
 EQCONV_API int eqconv_embedding(eqconv_plan_t plan, int64_t N, const void* ids, int id_bits, const void* table,
                                 int64_t table_stride, float scale, void* y, int64_t y_stride, eqconv_stream_t stream);
 
@@ -482,7 +483,8 @@ EQCONV_API size_t eqconv_embedding_workspace_bytes(eqconv_plan_t plan, int64_t N
  * 0 for the padding row and for types no node has; ids out of range set the
  * status word and add nothing.  The nodes are ordered by type first (stable)
  * and summed in fp32 in an order that depends on the sizes and ids alone:
- * bitwise reproducible, no atomics on values.  All of dT is overwritten. */
+ * bitwise reproducible, no atomics on values.  All of dT is overwritten; it
+ * overlaps neither gy nor ids. */
 EQCONV_API int eqconv_embedding_backward(eqconv_plan_t plan, int64_t N, const void* ids, int id_bits, const void* gy,
                                          int64_t gy_stride, float scale, void* dtable, void* workspace,
                                          size_t workspace_bytes, eqconv_stream_t stream);
@@ -508,7 +510,9 @@ EQCONV_API int eqconv_block_norm_plan_create(eqconv_plan_t* out, const char* irr
 
 /* The forward; one launch on `stream`.  stats [2][N][L+1] fp32 receives
  * 1 / rms(b) and 1 / rms(x_out) for the backward (null: not kept; the half of
- * an absent norm is not written).  Outputs overlap no input. */
+ * an absent norm is not written).  Outputs overlap no input.  Here and in the
+ * backward a bounded wait for a copy that gives up sets the status word (bit
+ * 4); the results are then unspecified. */
 EQCONV_API int eqconv_block_norm(eqconv_plan_t plan, int N, const void* x, const void* b, const void* gate,
                                  const float* w_post, const float* w_pre, float scale, void* x_out, void* h,
                                  float* stats, eqconv_stream_t stream);
