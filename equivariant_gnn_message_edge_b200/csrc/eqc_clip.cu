@@ -209,7 +209,9 @@ int64_t chunks_of(const eqconv_tensor_t& t) {
 
 inline int blocks_for(int64_t chunks, int per_sm) { return (int)(chunks < 148 * per_sm ? chunks : 148 * per_sm); }
 
-// Tensors [from, to) of one launch: at most MAXT, and 2^30 chunks.
+// Tensors [from, to) of one launch: at most MAXT that have elements, and 2^30
+// chunks.  Empty tensors behind the last one belong to the same launch, so that
+// every table but an empty list's has a tensor.
 template <int MAXT>
 int fill(Table<MAXT>& t, int n, const eqconv_tensor_t* ts, int from) {
     int64_t chunks = 0;
@@ -227,6 +229,7 @@ int fill(Table<MAXT>& t, int n, const eqconv_tensor_t* ts, int from) {
         t.type[t.count] = (uint8_t)ts[i].type;
         t.chunk0[++t.count] = (int)chunks;
     }
+    while (i < n && chunks_of(ts[i]) == 0) ++i;
     return i;
 }
 

@@ -556,6 +556,28 @@ def test_clip(case, bound):
     assert torch.equal(n, n2) and all(torch.equal(t, o) for t, o in zip(ts, outs))
 
 
+@pytest.mark.parametrize("empties", ["none", "leading", "between", "trailing"])
+@pytest.mark.parametrize("count", [1023, 1024, 1025, 2048])
+def test_clip_lists_around_a_launch(count, empties):
+    """Lists of as many tensors as one launch takes, and one more or fewer, with
+    empty tensors at either end or between: all are clipped, in place and not."""
+    ts = _tensors([1 + i % 5 for i in range(count)], ["bf16" if i % 7 == 3 else "fp32" for i in range(count)], seed=count)
+    none = [torch.zeros(0, device="cuda") for _ in range(3)]
+    if empties == "between":
+        ts = [t for i, t in enumerate(ts) for t in ([none[0], t] if i % 100 == 50 else [t])]
+    ts = none * (empties == "leading") + ts + none * (empties == "trailing")
+    want_n, want = ol.clip([np64(t) for t in ts], 0.5, np.float32(1e-6).astype(np.float64))
+    outs = [torch.full_like(t, float("nan")) for t in ts]
+    n = layers.clip_gradients(ts, 0.5, out=outs)
+    # roundings as in test_clip
+    assert abs(n.item() - want_n) <= 2 * U * want_n
+    for o, w in zip(outs, want):
+        assert_within("out", o, w, (3 * U + half(o.dtype)) * np.abs(w) * (1 + 1e-3) + tiny(o.dtype))
+    n2 = layers.clip_gradients(ts, 0.5)
+    assert torch.equal(n, n2) and all(torch.equal(t, o) for t, o in zip(ts, outs))
+    assert abs(layers.gradient_norm(ts).item() - 0.5) <= 0.5 * 2.0 ** -7
+
+
 def test_clip_range_of_values():
     """Squares that fp32 cannot hold, large and small, still give the norm."""
     for v in (1e-30, 1e30, 3e38, 1e-44):
