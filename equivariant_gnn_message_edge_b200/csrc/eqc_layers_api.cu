@@ -115,11 +115,14 @@ int norm_args(eqconv_plan_t plan, int N, const void* x, const void* b, const voi
     return EQCONV_OK;
 }
 
+// A tensor fits one launch (2^30 chunks of 32 KB, its start up to 15 bytes into the first).
+constexpr int64_t kMaxTensorBytes = (int64_t(1) << 45) - 16;
+
 int check_tensors(int n, const eqconv_tensor_t* t) {
     if (n < 0 || (n > 0 && !t)) return EQCONV_ERR_INVALID_ARG;
     for (int i = 0; i < n; ++i) {
         const size_t es = type_bytes(t[i].type);
-        if (!es || t[i].n < 0 || t[i].n > (int64_t(1) << 44)) return EQCONV_ERR_INVALID_ARG;
+        if (!es || t[i].n < 0 || t[i].n > kMaxTensorBytes / (int64_t)es) return EQCONV_ERR_INVALID_ARG;
         if (t[i].n > 0 && (!t[i].in || !aligned_to(t[i].in, es))) return EQCONV_ERR_INVALID_ARG;
     }
     return EQCONV_OK;

@@ -533,8 +533,8 @@ EQCONV_API int eqconv_block_norm_backward(eqconv_plan_t plan, int N, const void*
                                           float* dw_post, float* dw_pre, void* workspace, size_t workspace_bytes,
                                           eqconv_stream_t stream);
 
-/* One tensor of a list: n elements at `in` (contiguous), of a type code; the
- * scaled elements go to `out` (which may be `in`). */
+/* One tensor of a list: n elements at `in` (contiguous, 2^45 - 16 bytes at
+ * most), of a type code; the scaled elements go to `out` (which may be `in`). */
 typedef struct eqconv_tensor_s {
     const void* in;
     void* out;

@@ -104,6 +104,20 @@ def test_clip_workspace():
     assert B.eqconv_clip_workspace_bytes(m, bad) == 0
 
 
+@pytest.mark.parametrize("n,type_", [(2 ** 45 // 4, 0), (2 ** 45 // 4 - 3, 0), (2 ** 45 // 2, 1), (2 ** 62, 2)])
+def test_clip_refuses_tensors_beyond_a_launch(n, type_):
+    """A tensor that no launch could take is refused, not looked for without end."""
+    arr, m = _list((BASE, BASE, n, type_))
+    assert B.eqconv_clip_workspace_bytes(m, arr) == 0
+    for call in (lambda: B.eqconv_gradient_norm(m, arr, BASE * 4, BASE * 8, 1 << 30, 0),
+                 lambda: B.eqconv_clip_gradients(m, arr, 1.0, 1e-6, BASE * 4, BASE * 8, 1 << 30, 0)):
+        with pytest.raises(B.EqconvError) as e:
+            call()
+        assert e.value.status == B.EQCONV_ERR_INVALID_ARG
+    ok, m = _list((BASE + 4, BASE + 4, 2 ** 45 // 4 - 4, 0))            # the longest, off the 16-byte boundary
+    assert B.eqconv_clip_workspace_bytes(m, ok) > 0
+
+
 def test_python_refusals():
     with pytest.raises(TypeError):
         layers.clip_gradients(torch.zeros(3), 1.0)
