@@ -53,11 +53,19 @@ struct Pack {
             s = __ldg(reinterpret_cast<const uint16_t*>(p));
         }
     }
-    // as load, for memory that the same kernel also writes
+    // as load, for memory that the same kernel also writes, or that the kernel
+    // before it writes while this one already waits (launch_after)
     __device__ __forceinline__ void load_rw(const T* p) {
-        static_assert(kPiece == 16, "whole 16-byte pieces");
+        if constexpr (kPiece == 16) {
 #pragma unroll
-        for (int i = 0; i < kBytes / 16; ++i) q[i] = reinterpret_cast<const uint4*>(p)[i];
+            for (int i = 0; i < kBytes / 16; ++i) q[i] = reinterpret_cast<const uint4*>(p)[i];
+        } else if constexpr (kPiece == 8) {
+            d = *reinterpret_cast<const uint2*>(p);
+        } else if constexpr (kPiece == 4) {
+            w = *reinterpret_cast<const uint32_t*>(p);
+        } else {
+            s = *reinterpret_cast<const uint16_t*>(p);
+        }
     }
     __device__ __forceinline__ void store(T* p) const {
         if constexpr (kPiece == 16) {
@@ -166,6 +174,8 @@ __device__ __forceinline__ void store2(T* p, const F2 (&v)[V / 2]) {
 // their places on the SMs while the last CTAs of this one still run
 // (let_next_start), and wait there until it has ended and its writes are seen
 // (wait_for_last, before anything else).  launch_after starts such a next one.
+// What the kernel before it wrote is read by plain loads: a read-only load
+// (__ldg) asks for memory that nobody writes as long as its kernel lives.
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;"); }
 __device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

@@ -368,7 +368,7 @@ constexpr int kZeroRows = 256, kZeroBytes = 512 * 1024;
 constexpr int64_t kSortZeroBytes = 64 << 20;
 
 struct SumParams {
-    const int *keys, *perm;   // nodes in type order
+    const int *keys, *perm;   // nodes in type order, as the kernel before left them
     int N, C, R, tiles, slabs, lx_log2;
     int sum_blocks, zero_rows;
     int64_t V, ldg, zero_from;     // rows up to zero_from are zeros already
@@ -381,7 +381,7 @@ __device__ __forceinline__ int lower_bound(const int* keys, int n, int k) {
     int lo = 0, hi = n;
     while (lo < hi) {
         const int mid = (int)(((unsigned)lo + (unsigned)hi) >> 1);
-        if (__ldg(keys + mid) < k) lo = mid + 1;
+        if (keys[mid] < k) lo = mid + 1;
         else hi = mid;
     }
     return lo;
@@ -427,8 +427,8 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const SumParams p, const
     const int n = (int)(p.N - q0 < p.R ? p.N - q0 : p.R);
     const int *keys = p.keys + q0, *perm = p.perm + q0;
     const int none = (int)p.V;
-    int cur = __ldg(keys);
-    bool begun_before = tile > 0 && __ldg(keys - 1) == cur;
+    int cur = keys[0];
+    bool begun_before = tile > 0 && keys[-1] == cur;
     float acc[VE];
 #pragma unroll
     for (int e = 0; e < VE; ++e) acc[e] = 0.f;
@@ -451,8 +451,8 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const SumParams p, const
     const auto fetch = [&](int j0) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            key[u] = j0 + u < n ? __ldg(keys + j0 + u) : none;
-            at[u] = j0 + u < n ? __ldg(perm + j0 + u) : 0;
+            key[u] = j0 + u < n ? keys[j0 + u] : none;
+            at[u] = j0 + u < n ? perm[j0 + u] : 0;
         }
     };
     fetch(0);
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const SumParams p, const
         if (cur == none) return;
     }
     if (begun_before) partial(0);
-    else if (q0 + n < p.N && __ldg(keys + n) == cur) partial(1);
+    else if (q0 + n < p.N && keys[n] == cur) partial(1);
     else row(cur);
 }
 
@@ -509,14 +509,14 @@ __global__ void __launch_bounds__(256) embed_join_kernel(const SumParams p, T* d
     const auto channel_of = [&](unsigned worker) { return (((int)(worker / tiles) << p.lx_log2) + x) * VE; };
     const auto type_of = [&](int tile) {
         const int64_t end = (int64_t)(tile + 1) * p.R;
-        const int k = __ldg(p.keys + end - 1), next = __ldg(p.keys + end);
-        const bool before = tile > 0 && __ldg(p.keys + end - p.R - 1) == k;
+        const int k = p.keys[end - 1], next = p.keys[end];
+        const bool before = tile > 0 && p.keys[end - p.R - 1] == k;
         return next == k && !before ? k : (int)p.V;
     };
-    const auto starts = [&](int64_t t, int k) { return t * p.R < p.N && __ldg(p.keys + t * p.R) == k; };
+    const auto starts = [&](int64_t t, int k) { return t * p.R < p.N && p.keys[t * p.R] == k; };
     const auto add = [&](float (&acc)[VE], int64_t row, int c) {
         Pack<float, VE> v;
-        v.load(p.part + row * p.C + c);
+        v.load_rw(p.part + row * p.C + c);
 #pragma unroll
         for (int e = 0; e < VE; ++e) acc[e] += v.e[e];
     };

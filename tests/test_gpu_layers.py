@@ -161,6 +161,31 @@ def test_embedding_gradient_tables(V):
     assert torch.equal(d, torch.zeros(V, C, device="cuda").index_add_(0, z, gy))
 
 
+@pytest.mark.parametrize("N", [16385, 40000])
+@pytest.mark.parametrize("V", [262143, 262144, 300000, 5000000, 2 ** 27 + 3])
+def test_embedding_gradient_of_many_passes(N, V):
+    """Tables whose ids take two, three and four passes of the tiled sort, with
+    padding and bad ids, in calls that follow one another in one workspace
+    (exact: small whole numbers)."""
+    C, pad = (4, 7) if V < 2 ** 27 else (1, 7)
+    op = layers.Embedding(V, C, padding=pad)
+    ws = torch.empty(B.eqconv_embedding_workspace_bytes(op.plan, N), dtype=torch.uint8, device="cuda")
+    g = gen(V + N)
+    calls = []
+    for k in range(4):
+        z = torch.randint(0, V, (N,), device="cuda", generator=g)
+        z[1::2] = z[1::2] // (V // 300) * (V // 300) % V                    # half of them share 300 rows
+        z[:5] = torch.tensor([0, V - 1, pad, -1, V], device="cuda")
+        calls.append((z, torch.randint(-4, 5, (N, C), device="cuda", generator=g).float()))
+    outs = [torch.full((V, C), float("nan"), device="cuda") for _ in calls]
+    for (z, gy), out in zip(calls, outs):
+        op.backward_raw(z, gy, out=out, workspace=ws)
+    for (z, gy), out in zip(calls, outs):
+        keep = (z >= 0) & (z < V) & (z != pad)
+        assert torch.equal(out, torch.zeros(V, C, device="cuda").index_add_(0, z[keep], gy[keep]))
+    assert B.eqconv_get_device_error(op.plan) == B.EQCONV_ERR_DEVICE_CHECK
+
+
 def test_embedding_bad_ids():
     for dtype, bad in ((torch.int32, [-1, 7, 2 ** 31 - 1, -2 ** 31]), (torch.int64, [-1, 7, 2 ** 40, -2 ** 62, 2 ** 32])):
         z = torch.tensor([0, 6] + bad + [3], dtype=dtype, device="cuda")
