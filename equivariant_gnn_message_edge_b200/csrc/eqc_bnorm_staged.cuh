@@ -70,8 +70,18 @@ __device__ __forceinline__ void fill(const StagedParams& s, const Ring& r, int k
     if (g >= s.total || lane >= s.tensors) return;
     const Window w = window(s, lane, g);
     const int slot = k % s.slots;
-    bulk::expect(r.full + slot, w.inside ? w.bytes : 0);
+    bulk::expect(r.full + slot, w.inside ? w.bytes + EQC_TEST_BULK_DEFICIT : 0);
     if (w.inside) bulk::copy(r.base + (int64_t)slot * s.slot_bytes + s.offset[lane], w.at, w.bytes, r.full + slot);
+}
+
+// What a worker that gave up at sequence number k does (by one thread, when all
+// of them have left their loop): reports it, and waits, each time within the
+// limit, for the copies on their way, so that they end before the CTA's memory
+// does.  They are those of k and of the worker's next numbers, `step` apart, up
+// to a ring's length.
+__device__ __forceinline__ void give_up(const StagedParams& s, const Ring& r, int k, int step, int mine) {
+    atomicOr(s.status, 4u);
+    for (int j = k; j < mine && j < k + s.slots; j += step) bulk::wait(r.full + j % s.slots, (uint32_t)(j / s.slots) & 1u);
 }
 
 // How far into its first piece the nodes of a slot begin.
@@ -396,7 +406,6 @@ __global__ void __launch_bounds__(CTA ? 256 : BWD ? 256 : 512, 1) bn_staged_kern
         for (int i = 0; i < V / 2; ++i) dwo[l][i] = dwi[l][i] = F2(0.f);
     WorkerSum<BWD ? 3 * (L + 1) : L + 1> sum{red, width, 0};
     const int mine = s.total > blockIdx.x ? (int)((s.total - blockIdx.x + gridDim.x - 1) / gridDim.x) : 0;
-    bool ok = true;
     // a node's statistics are fetched while the worker's last node is worked on
     float sb_next[BWD ? L + 1 : 1], sy_next[BWD ? L + 1 : 1];
     const int each = CTA ? 1 : 32 / width;       // nodes a worker takes at a time
@@ -410,13 +419,13 @@ __global__ void __launch_bounds__(CTA ? 256 : BWD ? 256 : 512, 1) bn_staged_kern
     };
     if constexpr (BWD)
         if (worker < mine) fetch(first_of(worker));
-    for (int k = worker; k < mine; k += workers) {
+    int k = worker;
+    for (; k < mine; k += workers) {
         const int slot = k % s.slots;
-        if (!bulk::wait(full + slot, (uint32_t)(k / s.slots) & 1u)) {
-            atomicOr(s.status, 4u);
-            ok = false;
-            break;
-        }
+        // a worker's threads give up together: a warp's here, a CTA's at the barrier that ends the slot
+        const bool there = bulk::wait(full + slot, (uint32_t)(k / s.slots) & 1u);
+        if constexpr (!CTA)
+            if (!__all_sync(0xffffffffu, there)) break;
         if constexpr (APART)
             if (fill_ends<T>(s, ring, k, lane, CTA ? blockDim.x : 32)) {
                 if constexpr (CTA) __syncthreads();
@@ -448,16 +457,14 @@ __global__ void __launch_bounds__(CTA ? 256 : BWD ? 256 : 512, 1) bn_staged_kern
             }
         }
         // everyone has read the slot: its next copies may come
-        if constexpr (CTA) __syncthreads();
-        else __syncwarp();
+        if constexpr (CTA) {
+            if (!__syncthreads_and(there)) break;
+        } else {
+            __syncwarp();
+        }
         if (lane < 32) fill(s, ring, k + s.slots, lane);
     }
-    if (!ok) {
-        // the copies still in flight end before the CTA's memory does (each wait is bounded)
-        if (lane == 0)
-            for (int i = 0; i < s.slots; ++i) bulk::wait(full + i, 0), bulk::wait(full + i, 1);
-        return;
-    }
+    if (k < mine && lane == 0) give_up(s, ring, k, workers, mine);
     if constexpr (BWD) {
         float* part = p.part + (int64_t)blockIdx.x * 2 * (L + 1) * p.C;
         if constexpr (CTA) {
@@ -497,11 +504,12 @@ __global__ void __launch_bounds__(CTA ? 256 : BWD ? 256 : 512, 1) bn_staged_kern
 // of a channel is formed once and the weights stay in registers.
 
 // Sums of K values over the CTA; red: [2][K][16], zeros behind the last warp.
+// Returns whether `ok` holds for every thread.
 template <int K>
 struct CtaSum {
     float* red;
     int flip;
-    __device__ __forceinline__ void operator()(float (&v)[K]) {
+    __device__ __forceinline__ bool operator()(float (&v)[K], bool ok) {
 #pragma unroll
         for (int o = 16; o; o >>= 1)
 #pragma unroll
@@ -511,7 +519,7 @@ struct CtaSum {
         if ((threadIdx.x & 31) == 0)
 #pragma unroll
             for (int i = 0; i < K; ++i) r[i * 16 + (threadIdx.x >> 5)] = v[i];
-        __syncthreads();
+        ok = __syncthreads_and(ok);
 #pragma unroll
         for (int i = 0; i < K; ++i) {
             F2 q[4][2];
@@ -521,6 +529,7 @@ struct CtaSum {
                         add2(add2(q[2][0], q[2][1]), add2(q[3][0], q[3][1])))
                        .sum();
         }
+        return ok;
     }
 };
 
@@ -568,17 +577,12 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
         if (pre && n < p.N) sy_next = __ldg(p.stats + p.N + n);
     };
     if constexpr (BWD) fetch(blockIdx.x);
-    for (int k = 0, slot = 0, turn = 0; k < mine; ++k) {
+    int k = 0;
+    for (int slot = 0, turn = 0; k < mine; ++k) {
         const int64_t n = blockIdx.x + (int64_t)k * gridDim.x;
         float sb = sb_next, sy = sy_next;
         if constexpr (BWD) fetch(n + gridDim.x);
-        if (!bulk::wait(full + slot, (uint32_t)turn & 1u)) {
-            // give up: the copies still in flight end first (each wait is bounded)
-            atomicOr(s.status, 4u);
-            if (threadIdx.x == 0)
-                for (int i = 0; i < s.slots; ++i) bulk::wait(full + i, 0), bulk::wait(full + i, 1);
-            return;
-        }
+        const bool there = bulk::wait(full + slot, (uint32_t)turn & 1u);      // all give up together, at the first sums
         if constexpr (APART)
             if (fill_ends<T>(s, ring, k, threadIdx.x, blockDim.x)) __syncthreads();
         const unsigned char* base = ring.base + (int64_t)slot * s.slot_bytes;
@@ -620,7 +624,8 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
                             sa[j][i] = mul2(sa[j][i], wo[j][i]);
                         }
                 float total[1] = {v.sum()};
-                if constexpr (!BWD) sum(total);
+                if constexpr (!BWD)
+                    if (!sum(total, there)) break;
                 sb = rsqrtf(total[0] * inv_m + p.eps);
                 release();
             }
@@ -639,7 +644,8 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
                 }
             if (pre) {
                 float total[1] = {v.sum()};
-                if constexpr (!BWD) sum(total);
+                if constexpr (!BWD)
+                    if (!sum(total, there)) break;
                 sy = rsqrtf(total[0] * inv_m + p.eps);
                 if (!post) release();
                 const F2 s1(sy);
@@ -689,7 +695,8 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
                 }
             }
             float total[3] = {v0.sum(), v1.sum(), v2.sum()};
-            if constexpr (BWD) sum(total);
+            if constexpr (BWD)
+                if (!sum(total, there)) break;
             release();
             const float m1 = total[0] * inv_m * sy * sy * sy;           // with t's factor s_y
             const F2 n1(-m1), n2(-((total[2] - m1 * total[1]) * inv_m));
@@ -718,6 +725,7 @@ __global__ void __launch_bounds__(512, BWD || J * V > 8 ? 1 : 2) bn_row_kernel(c
             ++turn;
         }
     }
+    if (k < mine && threadIdx.x == 0) give_up(s, ring, k, 1, mine);
     if constexpr (BWD) {
         float* part = p.part + (int64_t)blockIdx.x * 2 * p.C;
 #pragma unroll

@@ -6,6 +6,14 @@
 
 #include <cstdint>
 
+// How long a wait goes on, and bytes that every phase expects above its copies' (test-only builds change them).
+#ifndef EQC_BULK_WAIT_LIMIT_NS
+#define EQC_BULK_WAIT_LIMIT_NS 2000000000ull   // 2 s
+#endif
+#ifndef EQC_TEST_BULK_DEFICIT
+#define EQC_TEST_BULK_DEFICIT 0
+#endif
+
 namespace eqc {
 namespace bulk {
 
@@ -32,7 +40,9 @@ __device__ __forceinline__ void copy(void* dst, const void* src, uint32_t bytes,
 // Orders this thread's writes to shared memory before copies issued behind the next barrier.
 __device__ __forceinline__ void fence_writes() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// Waits for the phase of `parity`; false after two seconds without it.
+// Waits for the phase of `parity`; false when the limit passed without it.
+// The limit is each thread's own: threads that go on together agree on the
+// outcome first (a vote of the warp, or of the CTA at its next barrier).
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
     const uint32_t a = smem_u32(bar);
     uint64_t t0 = 0;
@@ -49,7 +59,7 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
         uint64_t now;
         asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
         if (!t0) t0 = now;
-        else if (now - t0 > 2000000000ull) return false;
+        else if (now - t0 > EQC_BULK_WAIT_LIMIT_NS) return false;
     }
 }
 
