@@ -125,8 +125,8 @@ class Embedding:
     def forward_raw(self, ids, table, scale: float = 1.0, out=None, stream=None):
         """out: rows may be spaced, as x[:, 0, :] of node features [N][D][C]."""
         tp, ts = self._rows("table", table, (self.n_types, self.C), self.dtype)
-        if ts is None:
-            raise ValueError("table must have contiguous rows")
+        if ts is None or ts < self.C:
+            raise ValueError("table must have contiguous rows that do not overlap")
         with _on(self.device, stream):
             ids, bits = self._ids(ids)
             shape = ids.shape + (self.C,)
@@ -135,8 +135,8 @@ class Embedding:
                 op, os = out.data_ptr(), self.C
             else:
                 op, os = self._rows("out", out, shape, self.out_dtype)
-                if os is None:
-                    raise ValueError("out must have contiguous, evenly spaced rows")
+                if os is None or os < self.C:
+                    raise ValueError("out must have contiguous, evenly spaced rows that do not overlap")
             B.eqconv_embedding(self.plan, ids.numel(), ids.data_ptr(), bits, tp, ts, scale, op, os)
         return out
 
@@ -171,8 +171,8 @@ class _EmbeddingFn(torch.autograd.Function):
     def forward(ctx, op: Embedding, ids, table, scale):
         ctx.op, ctx.scale = op, scale
         ctx.save_for_backward(ids)
-        if table.dim() == 2 and table.stride(-1) != 1:
-            table = table.contiguous()
+        if table.dim() == 2 and (table.stride(1) != 1 or table.stride(0) < table.shape[1]):
+            table = table.contiguous()          # columns apart, or rows that repeat or overlap
         return op.forward_raw(ids, table, scale)
 
     @staticmethod

@@ -254,6 +254,30 @@ def test_embedding_autograd():
         d.sum().backward()
 
 
+def test_embedding_tables_of_repeated_and_overlapping_rows():
+    """Through autograd a table may be any view: one row for all types, rows that
+    overlap, columns apart.  The raw form, which copies nothing, refuses them."""
+    V, C = 6, 8
+    op = layers.Embedding(V, C)
+    z = torch.randint(0, V, (50,), device="cuda", generator=gen(1))
+    w = torch.randint(-3, 4, (50, C), device="cuda", generator=gen(2)).float()
+    views = {"repeated": (torch.randn(1, C, device="cuda"), lambda t: t.expand(V, C)),
+             "overlapping": (torch.randn(2 * V + C, device="cuda"), lambda t: t.as_strided((V, C), (2, 1))),
+             "columns apart": (torch.randn(V, 2 * C, device="cuda"), lambda t: t[:, ::2]),
+             "transposed": (torch.randn(C, V, device="cuda"), lambda t: t.t())}
+    for name, (leaf, view) in views.items():
+        leaf.requires_grad_(True)
+        y = op(z, view(leaf))
+        assert torch.equal(y, view(leaf)[z]), name
+        (got,) = torch.autograd.grad((y * w).sum(), leaf)
+        (want,) = torch.autograd.grad((view(leaf)[z] * w).sum(), leaf)
+        assert torch.equal(got, want), name                     # exact: whole numbers
+        with pytest.raises(ValueError, match="rows"):
+            op.forward_raw(z, view(leaf.detach()))
+    with pytest.raises(ValueError, match="rows"):
+        op.forward_raw(z, torch.zeros(V, C, device="cuda"), out=torch.zeros(1, C, device="cuda").expand(50, C))
+
+
 # ----------------------------------------------------------------- block norm
 
 NORM = [  # N, L, C, dtype, gate
