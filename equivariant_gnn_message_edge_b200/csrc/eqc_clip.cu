@@ -233,8 +233,14 @@ int fill(Table<MAXT>& t, int n, const eqconv_tensor_t* ts, int from) {
     return i;
 }
 
-// Short lists launch with 1.2 KB of parameters, long ones with 30 KB.
-constexpr int kFew = 40, kMany = 1024;
+// Lists of up to 96 tensors (the 2.8 KB of a few layers' gradients) launch with
+// small parameters, longer ones with 30 KB, which take the host 5 us more a
+// call.  Time of a call's two launches on the host, by list and limit:
+//                    18 tensors   41 to 96     97 to 128
+//   limit 40            5.1 us       9.9 us       9.8 us
+//   limit 96            4.8 us       4.6 us       9.5 us
+//   limit 128           5.7 us       5.4 us       5.5 us
+constexpr int kFew = 96, kMany = 1024;
 
 template <int MAXT>
 cudaError_t run(int n, const eqconv_tensor_t* ts, bool scale, float max_norm, float eps, float* norm, double* part,

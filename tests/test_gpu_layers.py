@@ -606,9 +606,9 @@ def test_clip(case, bound):
 
 
 @pytest.mark.parametrize("empties", ["none", "leading", "between", "trailing"])
-@pytest.mark.parametrize("count", [1023, 1024, 1025, 2048])
+@pytest.mark.parametrize("count", [40, 41, 96, 97, 1023, 1024, 1025, 2048])
 def test_clip_lists_around_a_launch(count, empties):
-    """Lists of as many tensors as one launch takes, and one more or fewer, with
+    """Lists of as many tensors as a launch takes, and one more or fewer, with
     empty tensors at either end or between: all are clipped, in place and not."""
     ts = _tensors([1 + i % 5 for i in range(count)], ["bf16" if i % 7 == 3 else "fp32" for i in range(count)], seed=count)
     none = [torch.zeros(0, device="cuda") for _ in range(3)]
