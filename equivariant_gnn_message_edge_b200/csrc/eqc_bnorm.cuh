@@ -63,8 +63,11 @@ __device__ __forceinline__ float rcp_fast(float x) {
 
 // a(g) and a'(g) of V gates (pairs), of one kind (EQCONV_GATE_*).  The error is
 // a few units in the last place of fp32, and |g| more of them through the
-// rounded argument of the power.  tanh is (1 - q) / (1 + q) of q = exp(-2 |g|),
-// and near 0, where that cancels, its Taylor series: for |g| < 0.25 up to a
+// rounded argument of the power, in a' too: where a is close to 1, 1 - a is
+// taken from the power and not from a.  For the sigmoid s = 1 / (1 + e) with
+// e = exp(-g), 1 - s = e s (1 where s is 0 and e infinite: min(NaN, 1)).  tanh is
+// (1 - q) / (1 + q) of q = exp(-2 |g|), 1 - tanh^2 is 4 q / (1 + q)^2, and near
+// 0, where the first cancels, tanh is its Taylor series: for |g| < 0.25 up to a
 // term below 2^-28 of the value.  16-bit gates take g itself below 2^-8, which
 // leaves 2^-17 of the value there and above: 2^-6 of their own type's rounding
 // or less, for a third fewer instructions in rows that these bound.
@@ -82,8 +85,10 @@ __device__ __forceinline__ void gate_values(int kind, const F2 (&g)[V / 2], F2 (
             float nx, ny, dx, dy, sx, sy, fx, fy;
             fma2(q, minus, one).split(nx, ny);
             add2(q, one).split(dx, dy);
-            fx = copysignf(nx * rcp_fast(dx), x);
-            fy = copysignf(ny * rcp_fast(dy), y);
+            dx = rcp_fast(dx);
+            dy = rcp_fast(dy);
+            fx = copysignf(nx * dx, x);
+            fy = copysignf(ny * dy, y);
             if constexpr (SHORT) {
                 a[i] = F2(fabsf(x) < 0x1p-8f ? x : fx, fabsf(y) < 0x1p-8f ? y : fy);
             } else {
@@ -95,7 +100,8 @@ __device__ __forceinline__ void gate_values(int kind, const F2 (&g)[V / 2], F2 (
                 fma2(mul2(g[i], g2), c, g[i]).split(sx, sy);
                 a[i] = F2(fabsf(x) < 0.25f ? sx : fx, fabsf(y) < 0.25f ? sy : fy);
             }
-            da[i] = fma2(mul2(a[i], minus), a[i], one);
+            const F2 d2(2.f * dx, 2.f * dy);
+            da[i] = mul2(mul2(q, d2), d2);
         }
     } else {
         F2 s[V / 2], r[V / 2];      // the sigmoid, and 1 minus it
@@ -103,8 +109,10 @@ __device__ __forceinline__ void gate_values(int kind, const F2 (&g)[V / 2], F2 (
         for (int i = 0; i < V / 2; ++i) {
             float x, y;
             g[i].split(x, y);
-            s[i] = F2(rcp_fast(1.f + exp2_fast(-kLog2e * x)), rcp_fast(1.f + exp2_fast(-kLog2e * y)));
-            r[i] = fma2(s[i], minus, one);
+            const float ex = exp2_fast(-kLog2e * x), ey = exp2_fast(-kLog2e * y);
+            const float sx = rcp_fast(1.f + ex), sy = rcp_fast(1.f + ey);
+            s[i] = F2(sx, sy);
+            r[i] = F2(fminf(ex * sx, 1.f), fminf(ey * sy, 1.f));
         }
         if (kind == 1) {
 #pragma unroll
@@ -113,10 +121,11 @@ __device__ __forceinline__ void gate_values(int kind, const F2 (&g)[V / 2], F2 (
                 da[i] = mul2(s[i], r[i]);
             }
         } else {
+            // s (1 + g (1 - s)): the error of 1 - s counts |g| times beside 1
 #pragma unroll
             for (int i = 0; i < V / 2; ++i) {
                 a[i] = mul2(g[i], s[i]);
-                da[i] = mul2(s[i], fma2(g[i], r[i], one));
+                da[i] = mul2(s[i], fma2(g[i], fma2(s[i], minus, one), one));
             }
         }
     }

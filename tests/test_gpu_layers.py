@@ -483,6 +483,42 @@ def test_block_norm_extreme_gates():
             assert np.abs(np64(a) - w).max() <= 1e-5 * np.abs(w).max() + 1e-6
 
 
+@pytest.mark.parametrize("kind", ["sigmoid", "silu", "tanh"])
+@pytest.mark.parametrize("dtype,L,C", [("fp32", 0, 64), ("fp32", 2, 41), ("fp32", 0, 1024), ("fp32", 0, 9000),
+                                       ("fp32", 3, 700), ("bf16", 1, 64), ("bf16", 0, 4096), ("fp16", 0, 520)])
+def test_block_norm_gradient_of_saturated_gates(kind, dtype, L, C):
+    """The gate's gradient is right relative to itself where the gate is close to
+    its limits, 0 and 1 (-1 and 1).
+
+    dgate = scale a'(g) sum_m t u with t = g_x.  In units of 2^-24, a'(g) is off
+    by 3 |g| (the argument of the power, 2 |g| log2 e, rounded, with a constant
+    that is rounded too), 4 (2^x), 4 (1/x, twice) and 6 (sums and products); u by
+    what 1 / rms and a dozen factors are."""
+    N, t = 5, T[dtype]
+    g = gen(C + L)
+    x, b, gx = (randn(g, N, (L + 1) ** 2, C, dtype=t) for _ in range(3))
+    gate = ((torch.rand(N, L + 1, C, device="cuda", generator=g) - 0.5) * 80).to(t)
+    gate[0, 0, :8] = torch.tensor([0.0, -0.25, 0.25, 1e-3, 40.0, -40.0, 17.5, -17.5], device="cuda").to(t)
+    wo = 1 + 0.3 * randn(g, L + 1, C)
+    op = layers.BlockNorm(natural_irreps(L), C, gate=kind, dtype=t)
+    _, _, stats = op.forward_raw(x, b, gate, wo, None, scale=0.6, save=True)
+    dgate = op.backward_raw(x, b, gate, wo, None, stats, gx, None, scale=0.6)[2]
+    q, b64, w64 = np64(gate), np64(b), np64(wo)
+    s, r = 1 / (1 + np.exp(-q)), 1 / (1 + np.exp(q))
+    da, mag = {"sigmoid": (s * r, s * r), "silu": (s * (1 + q * r), s * (1 + np.abs(q) * r)),
+               "tanh": (1 / np.cosh(q) ** 2,) * 2}[kind]
+    want, size = np.empty_like(q), np.empty_like(q)
+    for l in range(L + 1):
+        rows = slice(l * l, (l + 1) ** 2)
+        v = b64[:, rows]
+        u = v / np.sqrt((v ** 2).mean(axis=(1, 2), keepdims=True) + np.float64(np.float32(1e-6))) * w64[l]
+        tu = np64(gx)[:, rows] * u * np.float64(np.float32(0.6))
+        want[:, l], size[:, l] = da[:, l] * tu.sum(1), mag[:, l] * np.abs(tu).sum(1)
+    rel = _rms_err(L, C) + (12 + 14 + 3 * np.abs(q) + 2 * L + 4) * U
+    # (products of values below the normal range of fp32 may vanish on the way)
+    assert_within("dgate", dgate, want, rel * size + half(t) * np.abs(want) * (1 + 1e-3) + tiny(t) + 2.0 ** -120)
+
+
 @pytest.mark.parametrize("N,L,C", [(21, 1, 64), (100, 1, 7), (1, 0, 1), (40, 0, 3), (9, 0, 4001), (700, 2, 33)])
 def test_block_norm_unaligned_views(N, L, C):
     """Tensors that start off the 16-byte boundary, each by its own step, give
