@@ -11,12 +11,11 @@ cudaError_t EQC_BN_NAME(BnParams& p, const Shape& s, bool bwd, cudaStream_t st) 
     const float rows[4] = {1.f, 3.f, 5.f, 7.f};
     split_ctas(p, kStreamCtas, rows);
     if (bwd) {
+        // the kernel's limit is set once and for every C: threads that call at once must not lower each other's
+        static bool done[64] = {};
+        const cudaError_t e = allow_smem(bn_bwd_stream<T>, done);
+        if (e != cudaSuccess) return e;
         const int smem = 2 * p.C * (int)sizeof(float);
-        if (smem > 40 * 1024) {
-            const cudaError_t e =
-                cudaFuncSetAttribute(bn_bwd_stream<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-            if (e != cudaSuccess) return e;
-        }
         bn_bwd_stream<T><<<p.first[p.L + 1], 256, smem, st>>>(p);
     } else {
         bn_fwd_stream<T><<<p.first[p.L + 1], 256, 0, st>>>(p);

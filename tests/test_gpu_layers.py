@@ -7,6 +7,8 @@ finfo(t).eps / 2 relative to itself; HALF counts that.  What comes before it is
 fp32 (or wider) arithmetic, whose error is bounded by its longest chain of
 operations: a sum of n terms by warps and threads is off by less than
 n 2^-24 sum |terms| (any order), and in practice by far less."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -844,6 +846,43 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for k, r in got:
         assert all(torch.equal(a, c) for a, c in zip(r, want[k]))
+
+
+def test_two_host_threads_at_once():
+    """Rows of different widths through one kernel, from two host threads with a
+    stream each: neither changes what the other's launches may take."""
+    widths = (8196, 16384)                       # too wide for registers, 66 and 131 KB of shared memory backward
+    cases = []
+    for C in widths:
+        x, b, gate, wo, wi, gx, gh = _norm_case(1, 0, C, "fp32", "sigmoid", seed=C)
+        op = layers.BlockNorm("0e", C)
+        stats = op.forward_raw(x, b, gate, wo, wi, save=True)[2]
+        want = op.backward_raw(x, b, gate, wo, wi, stats, gx, gh)
+        got = [torch.zeros_like(t) for t in want]
+        ws = torch.empty(B.eqconv_block_norm_workspace_bytes(op.plan, 1), dtype=torch.uint8, device="cuda")
+        p = [t.data_ptr() for t in (x, b, gate, wo, wi, stats, gx, gh, *got)]
+        cases.append((op, p, ws, got, want, (x, b, gate, wo, wi, stats, gx, gh)))
+    torch.cuda.synchronize()
+    wrong, start = [], threading.Barrier(2)
+
+    def run(op, p, ws, got, want, inputs):
+        try:
+            stream = torch.cuda.Stream()
+            start.wait()
+            for _ in range(3000):
+                B.eqconv_block_norm_backward(op.plan, 1, *p[:5], 1.0, *p[5:], ws, ws.numel(), stream.cuda_stream)
+            stream.synchronize()
+            if not all(torch.equal(a, c) for a, c in zip(got, want)):
+                wrong.append("results")
+        except Exception as e:
+            wrong.append(repr(e))
+
+    threads = [threading.Thread(target=run, args=c) for c in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
 
 
 def test_clip_counts_as_in_place():
