@@ -92,6 +92,9 @@ class Embedding:
                                                    -1 if padding is None else padding)
         self.device = torch.cuda.current_device()
 
+    def __reduce__(self):       # a copy has a plan of its own, on the device that is current where it is made
+        return type(self), (self.n_types, self.C, self.dtype, self.out_dtype, self.padding)
+
     def __del__(self):
         try:
             B.eqconv_plan_destroy(self.plan)
@@ -201,6 +204,9 @@ class BlockNorm:
         self.device = torch.cuda.current_device()
         self.D = B.eqconv_plan_info(self.plan)["D_in"]
         self.L = int(round(self.D ** 0.5)) - 1
+
+    def __reduce__(self):       # as the embedding's
+        return type(self), (self.irreps, self.C, self.gate, self.eps, self.dtype)
 
     def __del__(self):
         try:

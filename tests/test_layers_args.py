@@ -1,6 +1,8 @@
 """The node-level operators' checks of their arguments, without a GPU: every
 refusal below comes before any device work."""
+import copy
 import ctypes
+import pickle
 
 import numpy as np
 import pytest
@@ -133,6 +135,36 @@ def test_python_refusals():
         layers.Embedding(4, 8, dtype=torch.float64)
     with pytest.raises(ValueError):
         layers.Embedding(4, 8, padding=4)
+
+
+def test_copies_have_plans_of_their_own(monkeypatch):
+    """Copied and pickled operators: no plan is destroyed twice or used after."""
+    alive, made = set(), []
+
+    def create(*args):
+        made.append(args)
+        alive.add(len(made))
+        return len(made)
+
+    monkeypatch.setattr(B, "eqconv_embedding_plan_create", create)
+    monkeypatch.setattr(B, "eqconv_block_norm_plan_create", create)
+    monkeypatch.setattr(B, "eqconv_plan_destroy", lambda plan: alive.remove(plan) if plan in alive else twice.append(plan))
+    monkeypatch.setattr(B, "eqconv_plan_info", lambda plan: {"D_in": 9})
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    twice = []
+    for op in (layers.Embedding(7, 12, torch.float32, torch.bfloat16, padding=3),
+               layers.BlockNorm("0e+1o+2e", 8, gate="silu", eps=1e-5, dtype=torch.float16)):
+        keep = [op]
+        for again in (copy.copy, copy.deepcopy, lambda o: pickle.loads(pickle.dumps(o))):
+            keep.append(again(op))
+            state = lambda o: {k: v for k, v in vars(o).items() if k != "plan"}  # noqa: E731
+            assert state(keep[-1]) == state(op) and made[-1] == made[op.plan - 1]
+        assert len({o.plan for o in keep}) == 4
+        del op, again
+        while keep:
+            assert all(o.plan in alive for o in keep)
+            keep.pop()
+    assert not alive and not twice and len(made) == 8
 
 
 def test_tensor_record_layout():
