@@ -786,8 +786,6 @@ inline Staged staged_shape(int64_t N, int L, int C, int es, int tensors, bool ga
         const int warps = s.slots < most ? s.slots : most;
         s.slots = s.slots / warps * warps;
         s.threads = 32 * warps;
-        // the reduction of the weight gradients takes threads * V floats of the ring
-        if (s.slots * slot(s.nodes) < (int64_t)s.threads * s.V * 4) return Staged{};
     } else if (L == 0) {
         // 8 channels a thread, 16 for the widest 16-bit rows; 512 threads an SM (128 registers each) backward and
         // for the widest, 1024 else
@@ -815,6 +813,9 @@ inline Staged staged_shape(int64_t N, int L, int C, int es, int tensors, bool ga
         s.slots = (int)(slots() < 4 ? slots() : 4);
     }
     s.smem = s.ring + (int)slot(s.nodes) * s.slots;
+    // where a warp has a node, the weight gradients are summed over the warps in the ring's place, which takes
+    // threads * V floats: 8 KB, more than the ring of the narrowest rows
+    if (bwd && s.width <= 32 && s.smem < s.ring + s.threads * s.V * 4) s.smem = s.ring + s.threads * s.V * 4;
     return s;
 }
 

@@ -55,7 +55,9 @@ extern "C" __attribute__((visibility("default"))) int eqc_probe_block_norm(int N
     return (int)eqc::block_norm_backward(a, static_cast<cudaStream_t>(stream));
 }
 
-// Whether the staged kernels take the case (aligned tensors).
-extern "C" __attribute__((visibility("default"))) int eqc_probe_block_norm_staged(int N, int L, int C, int backward) {
-    return eqc::bn::staged_shape(N, L, C, 2, backward ? 4 : 2, true, backward != 0, true).slots;
+// Whether the staged kernels take the case: `tensors` as large as x, of elements of `bytes`.
+extern "C" __attribute__((visibility("default"))) int eqc_probe_block_norm_staged(int N, int L, int C, int bytes,
+                                                                                  int tensors, int gated, int backward,
+                                                                                  int aligned) {
+    return eqc::bn::staged_shape(N, L, C, bytes, tensors, gated != 0, backward != 0, aligned != 0).slots;
 }

@@ -435,6 +435,17 @@ def test_block_norm(case, form):
     assert none is None and (xo is None or torch.equal(xo, xo2)) and (h is None or torch.equal(h, h2))
 
 
+@pytest.mark.parametrize("form", ["both", "post", "pre"])
+@pytest.mark.parametrize("case", [
+    (20000, 0, 33, "bf16", "silu"), (20000, 0, 32, "bf16", "tanh"), (200000, 0, 4, "bf16", "sigmoid"),
+    (10000, 0, 65, "fp16", "none"), (5000, 0, 130, "bf16", "silu"), (5000, 0, 33, "fp32", "sigmoid"),
+    (2000, 0, 96, "fp32", "none"), (9001, 0, 1, "bf16", "tanh"), (70, 0, 2, "fp16", "silu"), (3001, 0, 7, "fp32", "tanh"),
+    (3000, 1, 1, "bf16", "sigmoid"), (777, 2, 3, "fp32", "silu")], ids=str)
+def test_block_norm_narrow_rows(case, form):
+    """Rows of few channels, whose ring of slots is small."""
+    test_block_norm(case, form)
+
+
 @pytest.mark.parametrize("missing", ["g_x", "g_h"])
 def test_block_norm_one_gradient_only(missing):
     case = (40, 2, 64, "fp32", "sigmoid")

@@ -37,7 +37,7 @@ def test_waits_that_cannot_end(N, L, C):
     lib = ctypes.CDLL(PROBE)
     run = lib.eqc_probe_block_norm
     run.argtypes = [ctypes.c_int] * 4 + [ctypes.c_void_p] * 2
-    assert lib.eqc_probe_block_norm_staged(N, L, C, 0) and lib.eqc_probe_block_norm_staged(N, L, C, 1)
+    assert all(lib.eqc_probe_block_norm_staged(N, L, C, 2, t, 1, back, 1) for t, back in ((2, 0), (4, 1)))
     g = torch.Generator(device="cuda").manual_seed(N + C)
     bf = lambda *s: torch.randn(*s, device="cuda", generator=g).to(torch.bfloat16)  # noqa: E731
     x, b, gx, gh = (bf(N, (L + 1) ** 2, C) for _ in range(4))

@@ -2,6 +2,7 @@
 refusal below comes before any device work."""
 import copy
 import ctypes
+import os
 import pickle
 
 import numpy as np
@@ -165,6 +166,24 @@ def test_copies_have_plans_of_their_own(monkeypatch):
             assert all(o.plan in alive for o in keep)
             keep.pop()
     assert not alive and not twice and len(made) == 8
+
+
+@pytest.mark.parametrize("tensors,gated,backward", [(1, 0, 0), (2, 0, 0), (2, 1, 0),              # forward
+                                                    (1, 0, 1), (2, 0, 1), (3, 1, 1), (4, 1, 1)])    # backward
+@pytest.mark.parametrize("es", [2, 4])
+def test_narrow_nodes_are_staged(es, tensors, gated, backward):
+    """Nodes of few channels take the block norm's staged kernels, aligned or
+    not, however few tensors a call has: the others are for nodes too large."""
+    probe = os.path.join(os.path.dirname(os.path.abspath(B.__file__)), "libeqc_bulk_wait_probe.so")
+    assert os.path.exists(probe), "not built (python -m equivariant_gnn_message_edge_b200.build_lib)"
+    staged = ctypes.CDLL(probe).eqc_probe_block_norm_staged
+    for C in [*range(1, 40), 63, 64, 65, 96, 100, 127, 128, 129, 130, 200, 255, 256]:
+        for N in (1, 100, 5000, 20000, 200000):
+            for L in (0, 1, 2):
+                if L and C > 64:
+                    continue
+                for aligned in (0, 1):
+                    assert staged(N, L, C, es, tensors, gated, backward, aligned) >= 1, (N, L, C, aligned)
 
 
 def test_tensor_record_layout():
