@@ -646,13 +646,13 @@ struct Shape {
 
 // Groups that fit a CTA's registers: 16 bytes a thread and row in one piece,
 // four for L = 0 (rows wider than the staged kernels take: up to 512 threads),
-// and for the fp32 backward at L = 3 also 8 bytes (rows of no whole 16 bytes of
-// which two nodes do not fit shared memory).  pieces: bytes all rows start on.
+// and for the backward at L = 3 also 8 bytes (rows of no whole 16 bytes of which
+// two nodes do not fit shared memory).  pieces: bytes all rows start on.
 inline Shape shape_of(int L, int C, int es, bool bwd, int pieces) {
     Shape s{16 / es, L == 0 ? 4 : 1, 0};
     if (pieces % 16 != 0 || C * es % 16 != 0) {
-        if (!(L == 3 && es == 4 && bwd && pieces % 8 == 0 && C % 2 == 0)) return Shape{0, 0, 0};
-        s.V = 2;
+        if (!(L == 3 && bwd && pieces % 8 == 0 && C * es % 8 == 0)) return Shape{0, 0, 0};
+        s.V = 8 / es;
     }
     const int across = (C / s.V + s.J - 1) / s.J;
     if (across > (L == 0 ? 512 : 256) || (L == 1 && es == 4)) return Shape{0, 0, 0};
@@ -712,8 +712,8 @@ cudaError_t launch_for(BnParams& p, const Shape& s, cudaStream_t st) {
     if constexpr (W == 8)
         if (p.L == 1) return launch<T, W, 1, 1, BWD>(p, s, st);
     if (p.L == 2) return launch<T, W, 2, 1, BWD>(p, s, st);
-    if constexpr (W == 4 && BWD)
-        if (s.V == 2) return launch<T, 2, 3, 1, BWD>(p, s, st);
+    if constexpr (BWD)
+        if (s.V < W) return launch<T, W / 2, 3, 1, BWD>(p, s, st);
     return launch<T, W, 3, 1, BWD>(p, s, st);
 }
 

@@ -446,6 +446,15 @@ def test_block_norm_narrow_rows(case, form):
     test_block_norm(case, form)
 
 
+@pytest.mark.parametrize("form", ["both", "pre"])
+@pytest.mark.parametrize("case", [(60, 3, 820, "bf16", "silu"), (33, 3, 1020, "fp16", "none"), (40, 3, 1018, "bf16", "tanh")],
+                         ids=str)
+def test_block_norm_wide_nodes_in_8_byte_rows(case, form):
+    """16-bit nodes of which two do not fit shared memory backward, in rows of
+    whole 8 bytes and of 4."""
+    test_block_norm(case, form)
+
+
 @pytest.mark.parametrize("missing", ["g_x", "g_h"])
 def test_block_norm_one_gradient_only(missing):
     case = (40, 2, 64, "fp32", "sigmoid")
