@@ -175,7 +175,8 @@ __device__ __forceinline__ int degree_of(const BnParams& p, int cta) {
 
 // Streaming, for groups that fit neither shared memory nor registers: one CTA
 // walks nodes of one degree, three passes over a group's channels (the later
-// ones hit L1 or L2), and is bound by their latency.
+// ones hit L1 or L2), and is bound by their latency (3000 fp32 rows of 6001:
+// forward 350 us, backward 525 us; 3000 lmax3 nodes of 509: backward 486 us).
 template <class T>
 __global__ void __launch_bounds__(256) bn_fwd_stream(const BnParams p) {
     __shared__ float red[8];
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(256) bn_bwd_stream(const BnParams p) {
 // all loads of a batch are in flight together.  The weights and the sums of
 // their gradients stay in the thread that owns the channel for the whole
 // persistent loop over nodes.  3000 lmax3 nodes of 512 fp32 channels: backward
-// 203 us (3.1 TB/s), since loads, sums and stores of a group follow one another.
+// 198 us (3.2 TB/s), since loads, sums and stores of a group follow one another.
 
 // Sums of NB values over the worker's threads; every thread gets them.
 template <int NB>
@@ -647,7 +648,8 @@ struct Shape {
 // Groups that fit a CTA's registers: 16 bytes a thread and row in one piece,
 // four for L = 0 (rows wider than the staged kernels take: up to 512 threads),
 // and for the backward at L = 3 also 8 bytes (rows of no whole 16 bytes of which
-// two nodes do not fit shared memory).  pieces: bytes all rows start on.
+// two nodes do not fit shared memory: 3000 nodes of 1020 bf16 channels 338 us,
+// streaming 861 us).  pieces: bytes all rows start on.
 inline Shape shape_of(int L, int C, int es, bool bwd, int pieces) {
     Shape s{16 / es, L == 0 ? 4 : 1, 0};
     if (pieces % 16 != 0 || C * es % 16 != 0) {

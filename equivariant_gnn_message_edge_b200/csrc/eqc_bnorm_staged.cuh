@@ -13,9 +13,10 @@
 // or, for wide nodes, the whole CTA (one node a slot).  Its threads own V
 // channels of every row of the node.
 //
-// Bound by memory for fp32 (32768 lmax2 nodes of 128 channels: forward 107 us,
-// 6.1 TB/s; backward 167 us, 6.0 TB/s), by instructions for 16-bit elements
-// (the same nodes in bf16: 59 and 138 us).
+// Bound by memory for fp32 (32768 lmax2 nodes of 128 channels: forward 111 us,
+// 5.9 TB/s; backward 171 us, 5.9 TB/s).  16-bit nodes have half the bytes and
+// the same arithmetic, conversions and waits per element (the same nodes in
+// bf16: 56 us, 5.8 TB/s, and 133 us, 3.8 TB/s).
 #pragma once
 
 #include "eqc_bnorm.cuh"
@@ -499,9 +500,13 @@ __global__ void __launch_bounds__(CTA ? 256 : BWD ? 256 : 512, 1) bn_staged_kern
 // ---------------------------------------------------------------------------
 // Wide rows (L = 0, more than 32 vectors across): a CTA takes a row out of its
 // slot into registers (8 channels a thread), frees the slot at its first
-// barrier, and does all arithmetic from registers, once per element.  What
-// bounds it, beside memory, is the instructions per element, so every factor
-// of a channel is formed once and the weights stay in registers.
+// barrier, and does all arithmetic from registers, once per element: every
+// factor of a channel is formed once and the weights stay in registers.  fp32
+// rows are bound by memory (8191 x 4096: 116 and 165 us, 5.8 and 6.5 TB/s).
+// 16-bit rows (74 and 126 us, 4.5 and 4.3 TB/s) are bound by latency: a
+// scheduler has 8 warps forward and 4 backward, issues in 62 and 54 % of the
+// cycles, and they wait for shared memory, results and the barriers of the
+// row's sums; no pipe is busy for more than 37 %.
 
 // Sums of K values over the CTA; red: [2][K][16], zeros behind the last warp.
 // Returns whether `ok` holds for every thread.
@@ -755,7 +760,7 @@ inline Staged staged_shape(int64_t N, int L, int C, int es, int tensors, bool ga
     s.apart = !aligned || C * es % 16 != 0;
     s.batch = 1;
     // 16 bytes of neighbours a thread; 8 of 16-bit ones where more would not stay in registers (backward, L = 3:
-    // 16384 nodes of 128 bf16 channels 149 us, 194 us with 16 bytes), and four single channels where they lie apart
+    // 16384 nodes of 128 bf16 channels 146 us, 194 us with 16 bytes), and four single channels where they lie apart
     s.V = L == 0 || (!s.apart && (L <= 2 || !bwd)) ? 16 / es : 4;
     s.J = 1;
     const int vecs = (C + s.V - 1) / s.V;
@@ -769,7 +774,7 @@ inline Staged staged_shape(int64_t N, int L, int C, int es, int tensors, bool ga
         s.ctas = 1;
         s.ring = wbytes;
         // rows (L = 0) are small: so many a slot that the slots of all warps fill the shared memory, while there are
-        // rows for all (131072 fp32 rows of 128: forward 120 -> 81 us, backward 182 -> 138 us)
+        // rows for all (131072 fp32 rows of 128: 79 us forward and 135 us backward, with one row a slot 120 and 182 us)
         const int most = bwd ? 8 : 16, each = 32 / s.width;
         const int64_t full = (room - wbytes) / most / slot(each), some = N / ((int64_t)148 * most * each);
         s.batch = (int)(full < some ? full : some);

@@ -5,8 +5,8 @@
 // once for the scaling.  Squares are summed in fp64 (at the memory's rate an SM
 // has some 6 fp32 elements a clock to add, a tenth of what its fp64 units do),
 // so no gradient is so large or so small that its square leaves the range, and
-// the order of the sums is fixed.  564 MB of bf16 with some fp32: norm 102 us
-// (5.5 TB/s), scaling 178 us (6.3 TB/s, a part of the reads from L2).
+// the order of the sums is fixed.  564 MB of bf16 with some fp32: norm 100 us
+// (5.6 TB/s), norm and scaling 287 us (5.9 TB/s, a part of the reads from L2).
 #include <cuda_runtime.h>
 
 #include <cmath>

@@ -43,7 +43,7 @@ size_t block_norm_workspace(int L, int C, int N);
 cudaError_t block_norm_backward(const BlockNormArgs& a, cudaStream_t st);
 
 size_t clip_workspace(int n, const eqconv_tensor_t* t);
-// coefficient null: the norm alone
+// scale false: the norm alone
 cudaError_t clip_gradients(int n, const eqconv_tensor_t* t, bool scale, float max_norm, float eps, float* norm,
                            void* ws, cudaStream_t st);
 

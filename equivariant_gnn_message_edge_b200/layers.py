@@ -258,7 +258,8 @@ class BlockNorm:
     def backward_raw(self, x, b, gate, w_post, w_pre, stats, g_x, g_h, scale: float = 1.0, need_dw: bool = True,
                      workspace=None, stream=None):
         """(dx, db, dgate, dw_post, dw_pre) from the gradients of x_out and h
-        (None: zero); None in the places of inputs that are None."""
+        (None: zero); None in the places of inputs that are None, and for the
+        weights without ``need_dw``.  The others are always computed."""
         N, ptrs = self._inputs(x, b, gate, w_post, w_pre)
         dev = self.device
         if (g_x is not None and b is None) or (g_h is not None and w_pre is None):

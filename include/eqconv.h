@@ -482,9 +482,9 @@ EQCONV_API size_t eqconv_embedding_workspace_bytes(eqconv_plan_t plan, int64_t N
  *   dT[v, :] = scale * sum over nodes i with ids[i] = v of gy[i, :]
  * 0 for the padding row and for types no node has; ids out of range set the
  * status word and add nothing.  The nodes are ordered by type first (stable)
- * and summed in fp32 in an order that depends on the sizes and ids alone:
- * bitwise reproducible, no atomics on values.  All of dT is overwritten; it
- * overlaps neither gy nor ids. */
+ * and summed in fp32 in an order that depends on the sizes, the ids and the
+ * alignment of gy and dT alone: bitwise reproducible, no atomics on values.
+ * All of dT is overwritten; it overlaps neither gy nor ids. */
 EQCONV_API int eqconv_embedding_backward(eqconv_plan_t plan, int64_t N, const void* ids, int id_bits, const void* gy,
                                          int64_t gy_stride, float scale, void* dtable, void* workspace,
                                          size_t workspace_bytes, eqconv_stream_t stream);
@@ -525,8 +525,9 @@ EQCONV_API size_t eqconv_block_norm_workspace_bytes(eqconv_plan_t plan, int N);
  * dx, db, dgate (element type of the plan; dgate null without a gate) and
  * dw_post, dw_pre [L+1][C] fp32 (either may be null: not computed).  x_out is
  * formed again from x, b and gate; stats are the forward's.  The weight
- * gradients are summed in a fixed order: bitwise reproducible.  Outputs
- * overlap no input and are overwritten. */
+ * gradients are summed in an order that the sizes, the tensors given and their
+ * alignment fix: bitwise reproducible.  Outputs overlap no input and are
+ * overwritten. */
 EQCONV_API int eqconv_block_norm_backward(eqconv_plan_t plan, int N, const void* x, const void* b, const void* gate,
                                           const float* w_post, const float* w_pre, float scale, const float* stats,
                                           const void* g_x, const void* g_h, void* dx, void* db, void* dgate,
@@ -549,14 +550,16 @@ EQCONV_API size_t eqconv_clip_workspace_bytes(int n, const eqconv_tensor_t* tens
 
 /* *norm (device, fp32) = sqrt(sum over the list of all elements squared).
  * The list is read on the host during the call; `out` is not used.  Squares
- * are summed in fp64 in a fixed order.  These calls take no plan: the list
+ * are summed in fp64 in an order that the list and its tensors' alignment fix
+ * (16-bit ones in pairs added in fp32, or alone where those leave its range).  These calls take no plan: the list
  * and the workspace live on the current device. */
 EQCONV_API int eqconv_gradient_norm(int n, const eqconv_tensor_t* tensors, float* norm, void* workspace,
                                     size_t workspace_bytes, eqconv_stream_t stream);
 
 /* The norm as above, and out = k * in with k = min(1, max_norm / (norm + eps))
- * for every tensor.  In place, nothing is written when k = 1.  A norm that is
- * infinite gives k = 0, one that is NaN gives NaN everywhere.  max_norm >= 0,
+ * for every tensor, k formed in fp64 and rounded to fp32.  In place, nothing is
+ * written when k = 1.  An infinite element gives k = 0 (and itself becomes
+ * NaN), a NaN gives NaN everywhere.  max_norm >= 0,
  * eps > 0.  An output that overlaps another tensor of the list, or its own
  * input without being it, is refused (EQCONV_ERR_INVALID_ARG). */
 EQCONV_API int eqconv_clip_gradients(int n, const eqconv_tensor_t* tensors, float max_norm, float eps, float* norm,
